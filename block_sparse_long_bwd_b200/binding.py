@@ -7,6 +7,7 @@ status raises BBError.  The library is loaded on first use; if it is missing
 the call raises (there is no fallback of any kind).
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -41,6 +42,13 @@ class bb_attn_desc(ctypes.Structure):
                 ("dropout", ctypes.c_float), ("dropout_seed", ctypes.c_uint64),
                 ("mask_queries", ctypes.c_int), ("grad_fp32", ctypes.c_int),
                 ("dropout_bits", ctypes.c_void_p)]
+
+
+class bb_qk_desc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("L", ctypes.c_int),
+                ("d", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("theta", ctypes.c_double),
+                ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int)]
 
 
 _lib = None
@@ -100,6 +108,19 @@ def lib():
         L.bb_qkv_proj.restype = ctypes.c_int
         L.bb_out_proj.argtypes = [ctypes.c_int] * 4 + [_P] * 5 + [ctypes.c_size_t, _P]
         L.bb_out_proj.restype = ctypes.c_int
+        drop = [ctypes.c_uint64, ctypes.c_int, ctypes.c_float, ctypes.c_uint64,
+                ctypes.c_uint32]
+        L.bb_dropout_fwd.argtypes = drop + [_P] * 4
+        L.bb_dropout_fwd.restype = ctypes.c_int
+        L.bb_dropout_bwd.argtypes = drop + [_P] * 3
+        L.bb_dropout_bwd.restype = ctypes.c_int
+        qk = [ctypes.POINTER(bb_qk_desc)]
+        L.bb_qk_norm_rope_workspace_size.argtypes = qk + [ctypes.POINTER(ctypes.c_size_t)]
+        L.bb_qk_norm_rope_workspace_size.restype = ctypes.c_int
+        L.bb_qk_norm_rope_fwd.argtypes = qk + [_P] * 8
+        L.bb_qk_norm_rope_fwd.restype = ctypes.c_int
+        L.bb_qk_norm_rope_bwd.argtypes = qk + [_P] * 12 + [ctypes.c_size_t, _P]
+        L.bb_qk_norm_rope_bwd.restype = ctypes.c_int
         L.bb_attn_noalloc_status.argtypes = [_P]
         L.bb_attn_noalloc_status.restype = ctypes.c_int
         L.bb_attn_check_status.argtypes = [_P, _P]
@@ -336,6 +357,149 @@ def bb_out_proj(o, w_o, b_o, workspace, out=None, stream=None):
                              _ptr(workspace), workspace.numel() * workspace.element_size(),
                              _stream_ptr(stream)), "bb_out_proj")
     return out
+
+
+def _dtype_code(t, name):
+    code = {torch.float32: BB_F32, torch.bfloat16: BB_BF16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16")
+    return code
+
+
+def _like(t, name, ref, dtype=None):
+    """t, or a new tensor where it is None, shaped like ref (dtype: ref's
+    unless given)."""
+    dtype = ref.dtype if dtype is None else dtype
+    if t is None:
+        return torch.empty_like(ref, dtype=dtype)
+    _cuda_tensor(t, name, dtype)
+    _same_place(t, name, ref)
+    if t.shape != ref.shape:
+        raise ValueError(f"{name} must have shape {tuple(ref.shape)}")
+    return t
+
+
+def _same_place(t, name, ref):
+    if t.device != ref.device:
+        raise ValueError(f"{name} must be on {ref.device}")
+
+
+def _scope(ref, stream):
+    """Context of a call on ref's device and the given stream (None: that
+    device's current one), so that what the call allocates belongs to the
+    stream it runs on."""
+    if stream is not None:
+        if stream.device != ref.device:
+            raise ValueError(f"stream must be on {ref.device}")
+        return torch.cuda.stream(stream)
+    if ref.device.index != torch.cuda.current_device():
+        return torch.cuda.device(ref.device)
+    return contextlib.nullcontext()
+
+
+def bb_dropout_fwd(x, residual, rate, seed, site=0, out=None, stream=None):
+    """Output dropout with the residual added (see include/bb_attn.h):
+    x [...] bf16 or fp32, residual like x or None; returns out like x (out may
+    be x or residual)."""
+    _cuda_tensor(x, "x")
+    code = _dtype_code(x, "x")
+    if residual is not None:
+        _like(residual, "residual", x)
+    with _scope(x, stream):
+        out = _like(out, "out", x)
+        _check(lib().bb_dropout_fwd(x.numel(), code, rate, seed & ((1 << 64) - 1), site, _ptr(x),
+                                    _ptr(residual), _ptr(out), _stream_ptr(None)),
+               "bb_dropout_fwd")
+    return out
+
+
+def bb_dropout_bwd(dout, rate, seed, site=0, dx=None, stream=None):
+    """Gradient of bb_dropout_fwd's x (its residual's is dout); dx may be
+    dout."""
+    _cuda_tensor(dout, "dout")
+    code = _dtype_code(dout, "dout")
+    with _scope(dout, stream):
+        dx = _like(dx, "dx", dout)
+        _check(lib().bb_dropout_bwd(dout.numel(), code, rate, seed & ((1 << 64) - 1), site,
+                                    _ptr(dout), _ptr(dx), _stream_ptr(None)),
+               "bb_dropout_bwd")
+    return dx
+
+
+def make_qk_desc(B, H, L, dtype, eps=1e-6, theta=10000.0, rot_dim=64, interleaved=False, d=64):
+    """Descriptor of bb_qk_norm_rope_fwd / _bwd (see include/bb_attn.h)."""
+    if isinstance(dtype, torch.dtype):
+        dtype = {torch.float32: BB_F32, torch.bfloat16: BB_BF16}[dtype]
+    return bb_qk_desc(B, H, L, d, dtype, eps, theta, rot_dim, int(interleaved))
+
+
+def bb_qk_norm_rope_workspace_size(desc):
+    n = ctypes.c_size_t(0)
+    _check(lib().bb_qk_norm_rope_workspace_size(ctypes.byref(desc), ctypes.byref(n)),
+           "bb_qk_norm_rope_workspace_size")
+    return n.value
+
+
+def _qk_tensors(desc, tensors, gammas, positions):
+    """Checks of the tensors both passes read; tensors[0] sets the device."""
+    shape = (desc.B, desc.H, desc.L, desc.d)
+    dtype = torch.float32 if desc.dtype == BB_F32 else torch.bfloat16
+    ref = tensors[0][1]
+    for name, t in tensors:
+        _cuda_tensor(t, name, dtype)
+        _same_place(t, name, ref)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}")
+    for name, t in gammas:
+        if t is not None:
+            _cuda_tensor(t, name, torch.float32)
+            _same_place(t, name, ref)
+            if t.numel() != desc.d:
+                raise ValueError(f"{name} must have {desc.d} elements")
+    if positions is not None:
+        _cuda_tensor(positions, "positions", torch.int32)
+        _same_place(positions, "positions", ref)
+        if tuple(positions.shape) != (desc.B, desc.L):
+            raise ValueError(f"positions must have shape {(desc.B, desc.L)}")
+
+
+def bb_qk_norm_rope_fwd(desc, q, k, gamma_q, gamma_k, positions=None, q_out=None, k_out=None,
+                        stream=None):
+    """Per-head RMS norm and rotary rotation of q and k [B, H, L, 64] (see
+    include/bb_attn.h); gammas fp32 [64] or None, positions int32 [B, L] or
+    None; returns q_out, k_out (which may be q, k)."""
+    _qk_tensors(desc, (("q", q), ("k", k)), (("gamma_q", gamma_q), ("gamma_k", gamma_k)),
+                positions)
+    with _scope(q, stream):
+        q_out, k_out = _like(q_out, "q_out", q), _like(k_out, "k_out", k)
+        _check(lib().bb_qk_norm_rope_fwd(
+            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), _ptr(positions),
+            _ptr(q_out), _ptr(k_out), _stream_ptr(None)), "bb_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def bb_qk_norm_rope_bwd(desc, q, k, gamma_q, gamma_k, positions, dq_out, dk_out, dq=None, dk=None,
+                        workspace=None, stream=None):
+    """Gradients of bb_qk_norm_rope_fwd from its inputs q, k and upstream
+    dq_out, dk_out: returns dq, dk (which may be dq_out, dk_out) and dgamma_q,
+    dgamma_k fp32 [64].  workspace: uint8 of bb_qk_norm_rope_workspace_size
+    bytes, or None (allocated here)."""
+    _qk_tensors(desc, (("q", q), ("k", k), ("dq_out", dq_out), ("dk_out", dk_out)),
+                (("gamma_q", gamma_q), ("gamma_k", gamma_k)), positions)
+    with _scope(q, stream):
+        dq, dk = _like(dq, "dq", q), _like(dk, "dk", k)
+        dgamma = torch.empty((2, desc.d), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(bb_qk_norm_rope_workspace_size(desc), dtype=torch.uint8,
+                                    device=q.device)
+        _cuda_tensor(workspace, "workspace")
+        _same_place(workspace, "workspace", q)
+        _check(lib().bb_qk_norm_rope_bwd(
+            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), _ptr(positions),
+            _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dgamma[0]), _ptr(dgamma[1]),
+            _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _stream_ptr(None)), "bb_qk_norm_rope_bwd")
+    return dq, dk, dgamma[0], dgamma[1]
 
 
 def bb_attn_noalloc_status(stream=None):

@@ -17,6 +17,20 @@ constexpr int kMaxBlocks = 8192;   // nb limit (CSR builder keeps counts in smem
 constexpr int kMaxRand = 32;       // r limit (attended list fits in smem)
 constexpr float kLog2e = 1.4426950408889634f;
 
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+// Dropout rate in [0, 1), rounded to 1/256: the byte threshold and 1 / keep
+// probability.  False for a rate outside [0, 1) or one that rounds to 1
+// (it would drop everything: infinite scale).
+inline bool resolve_dropout(float rate, uint32_t* thr, float* scale) {
+  if (!(rate >= 0.f && rate < 1.f)) return false;
+  const int t = (int)((double)rate * 256.0 + 0.5);
+  if (t > 255) return false;
+  *thr = (uint32_t)t;
+  *scale = (float)(256.0 / (256.0 - t));
+  return true;
+}
+
 // Everything a kernel needs about one call, passed by value.
 struct Problem {
   int B, H, L, d, bs, r, nb, dtype;

@@ -240,12 +240,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
 }
 
-bool aligned16p(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 int launch_proj(ProjArgs pa, const void* a, uint64_t a_inner, uint64_t a_rows, const void* w,
                 void* o0, void* o1, void* o2, void* workspace, size_t ws_bytes, void* stream) {
   if (!workspace || ws_bytes < 256) return BB_ERR_WORKSPACE;
-  if (!aligned16p(workspace)) return BB_ERR_INVALID;
+  if (!aligned16(workspace)) return BB_ERR_INVALID;
   cudaStream_t s = (cudaStream_t)stream;
   pa.status = static_cast<int*>(workspace);
   CUtensorMap tmA, tmW, tmO0, tmO1, tmO2;
@@ -288,7 +286,7 @@ int bb_qkv_proj(int B, int L, int hidden, int H, const void* x, const void* w_qk
   if (!x || !w_qkv || !q || !k || !v) return BB_ERR_INVALID;
   const void* ptrs[] = {x, w_qkv, b_qkv, q, k, v};
   for (const void* p : ptrs)
-    if (!aligned16p(p)) return BB_ERR_INVALID;
+    if (!aligned16(p)) return BB_ERR_INVALID;
   // Tiles: 128 rows within one sequence, 256 columns within one of Q, K, V.
   if (L % kPBM != 0 || hidden % kPBK != 0 || (H * 64) % kPBN != 0) return BB_ERR_UNSUPPORTED;
   if ((uint64_t)B * H * L >= (1ull << 31) || (uint64_t)B * L * hidden >= (1ull << 31))
@@ -315,7 +313,7 @@ int bb_out_proj(int B, int L, int H, int hidden, const void* o, const void* w_o,
   if (!o || !w_o || !out) return BB_ERR_INVALID;
   const void* ptrs[] = {o, w_o, b_o, out};
   for (const void* p : ptrs)
-    if (!aligned16p(p)) return BB_ERR_INVALID;
+    if (!aligned16(p)) return BB_ERR_INVALID;
   if (L % kPBM != 0 || hidden % kPBN != 0) return BB_ERR_UNSUPPORTED;
   if ((uint64_t)B * H * L >= (1ull << 31) || (uint64_t)B * L * hidden >= (1ull << 31))
     return BB_ERR_UNSUPPORTED;

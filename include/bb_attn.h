@@ -266,6 +266,84 @@ BB_API int bb_out_proj(int B, int L, int H, int hidden, const void* o, const voi
                        const float* b_o, void* out, void* workspace, size_t workspace_bytes,
                        void* stream);
 
+/* Dropout of a layer's output, with the residual added in the same pass
+ * ([gitcode page] section "BigBirdEncoder 的关键参数", the encoder's dropout
+ * rate, and "梯度检查点的实现方式", stateless seeded dropout), over n elements in
+ * memory order:
+ *   out[i] = (residual[i] +) (keep(i) ? x[i] / keep probability : 0)
+ * computed in fp32 and rounded to the dtype once.  The rate is rounded to a
+ * multiple of 1/256 as bb_attn_desc.dropout is (thr, keep probability
+ * (256 - thr) / 256); a rate that rounds to 0 keeps everything.  keep(i) is a
+ * pure function of (seed, site, i), and no mask is stored: Philox4x32-10 with
+ * counter words ((i >> 4) mod 2^32, i >> 36, site, 2^32 - 1) and key words
+ * (seed mod 2^32, seed >> 32) gives 16 bytes, little-endian from its four
+ * output words in order, for elements 16 (i >> 4) .. + 15; byte i & 15 keeps
+ * the element when it is >= thr.  `site` tells apart the dropouts that share
+ * one seed (a layer index); the attention's own dropout never meets the same
+ * counters (its word 3 is a batch index).  A call captured into a graph
+ * replays the decisions of the captured seed and site.
+ *   n        elements, 1 .. 2^42
+ *   dtype    bb_dtype of every tensor
+ *   x        device
+ *   residual device, or NULL (nothing is added)
+ *   out      device (written); may be x or residual itself
+ * The gradient of x is bb_dropout_bwd(dout) with the forward's rate, seed and
+ * site; the gradient of residual is dout. */
+BB_API int bb_dropout_fwd(uint64_t n, int dtype, float rate, uint64_t seed, uint32_t site,
+                          const void* x, const void* residual, void* out, void* stream);
+
+/* Gradient of bb_dropout_fwd: dx[i] = keep(i) ? dout[i] / keep probability : 0,
+ * with the same decisions.  dx may be dout itself. */
+BB_API int bb_dropout_bwd(uint64_t n, int dtype, float rate, uint64_t seed, uint32_t site,
+                          const void* dout, void* dx, void* stream);
+
+/* RMS norm of each head's queries and keys with the rotary position rotation
+ * in the same pass, on tensors [B][H][L][d] as bb_qkv_proj writes and
+ * bb_attn_fwd reads them.  For a row x of d = 64 components at position p:
+ *   u = gamma * x / sqrt(mean(x^2) + eps)
+ *   y[a] = u[a] cos t_i - u[b] sin t_i,   y[b] = u[b] cos t_i + u[a] sin t_i
+ * for each pair i < rot_dim / 2 at angle t_i = p theta^(-2 i / rot_dim); pair
+ * i is (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved = 1.
+ * Components from rot_dim on are not rotated (rot_dim = 0: the norm alone).
+ * fp32 arithmetic, rounded to the dtype once; the angle is reduced to one
+ * turn exactly, so far positions are as accurate as near ones.
+ *   eps     >= 0
+ *   theta   >= 1 (ignored when rot_dim = 0); rot_dim even, 0 .. 64 */
+typedef struct {
+  int B, H, L, d;
+  int dtype;
+  float eps;
+  double theta;
+  int rot_dim;
+  int interleaved;
+} bb_qk_desc;
+
+/* Forward.
+ *   q, k              [B][H][L][64] dtype, device
+ *   gamma_q, gamma_k  [64] fp32, device, or NULL (ones)
+ *   positions         [B][L] int32, device (any value), or NULL (the index l)
+ *   q_out, k_out      [B][H][L][64] dtype, device (written); may be q and k
+ *                     themselves (the backward needs the original q and k) */
+BB_API int bb_qk_norm_rope_fwd(const bb_qk_desc* desc, const void* q, const void* k,
+                               const float* gamma_q, const float* gamma_k,
+                               const int32_t* positions, void* q_out, void* k_out, void* stream);
+
+/* Bytes of device workspace bb_qk_norm_rope_bwd needs (partial sums of the
+ * gamma gradients); written to *bytes.  Host only. */
+BB_API int bb_qk_norm_rope_workspace_size(const bb_qk_desc* desc, size_t* bytes);
+
+/* Backward: gradients for upstream dq_out, dk_out, from the forward's q and k
+ * (the norm is computed again).
+ *   dq, dk              [B][H][L][64] dtype, device (written); may be dq_out
+ *                       and dk_out themselves
+ *   dgamma_q, dgamma_k  [64] fp32, device (written), or NULL (not wanted)
+ *   workspace           device, 16-byte aligned; it holds no status word */
+BB_API int bb_qk_norm_rope_bwd(const bb_qk_desc* desc, const void* q, const void* k,
+                               const float* gamma_q, const float* gamma_k,
+                               const int32_t* positions, const void* dq_out, const void* dk_out,
+                               void* dq, void* dk, float* dgamma_q, float* dgamma_k,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
 /* Number of kernel launches bb_attn_fwd (pass 0) or bb_attn_bwd (pass 1)
  * makes for `desc`, written to *launches.  Host only. */
 BB_API int bb_attn_launch_count(const bb_attn_desc* desc, int pass,

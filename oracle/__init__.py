@@ -18,3 +18,11 @@ from .bigbird_oracle import (  # noqa: F401
     rand_table,
     random_candidates,
 )
+from .layer_oracle import (  # noqa: F401
+    linear_ce,
+    linear_ce_backward,
+    out_dropout,
+    out_dropout_keep,
+    qk_norm_rope,
+    qk_norm_rope_backward,
+)
