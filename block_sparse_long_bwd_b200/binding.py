@@ -20,11 +20,12 @@ BB_OK = 0
 BB_ERR_WORKSPACE = -4
 BB_ERR_TIMEOUT = -5
 BB_ERR_BAD_TABLE = -6
+BB_ERR_BAD_LABEL = -7
 BB_F32 = 0
 BB_BF16 = 1
 STATUS = {0: "BB_OK", -1: "BB_ERR_INVALID", -2: "BB_ERR_UNSUPPORTED",
           -3: "BB_ERR_CUDA", -4: "BB_ERR_WORKSPACE", -5: "BB_ERR_TIMEOUT",
-          -6: "BB_ERR_BAD_TABLE"}
+          -6: "BB_ERR_BAD_TABLE", -7: "BB_ERR_BAD_LABEL"}
 
 
 class BBError(RuntimeError):
@@ -121,6 +122,14 @@ def lib():
         L.bb_qk_norm_rope_fwd.restype = ctypes.c_int
         L.bb_qk_norm_rope_bwd.argtypes = qk + [_P] * 12 + [ctypes.c_size_t, _P]
         L.bb_qk_norm_rope_bwd.restype = ctypes.c_int
+        ce = [ctypes.c_int] * 3
+        L.bb_linear_ce_workspace_size.argtypes = ce + [ctypes.c_int,
+                                                       ctypes.POINTER(ctypes.c_size_t)]
+        L.bb_linear_ce_workspace_size.restype = ctypes.c_int
+        L.bb_linear_ce_fwd.argtypes = ce + [_P] * 7 + [ctypes.c_size_t, _P]
+        L.bb_linear_ce_fwd.restype = ctypes.c_int
+        L.bb_linear_ce_bwd.argtypes = ce + [_P] * 10 + [ctypes.c_size_t, _P]
+        L.bb_linear_ce_bwd.restype = ctypes.c_int
         L.bb_attn_noalloc_status.argtypes = [_P]
         L.bb_attn_noalloc_status.restype = ctypes.c_int
         L.bb_attn_check_status.argtypes = [_P, _P]
@@ -500,6 +509,91 @@ def bb_qk_norm_rope_bwd(desc, q, k, gamma_q, gamma_k, positions, dq_out, dk_out,
             _ptr(workspace), workspace.numel() * workspace.element_size(),
             _stream_ptr(None)), "bb_qk_norm_rope_bwd")
     return dq, dk, dgamma[0], dgamma[1]
+
+
+def bb_linear_ce_workspace_size(N, hidden, V, pass_):
+    n = ctypes.c_size_t(0)
+    _check(lib().bb_linear_ce_workspace_size(N, hidden, V, pass_, ctypes.byref(n)),
+           "bb_linear_ce_workspace_size")
+    return n.value
+
+
+def _ce_tensors(h, w, bias, labels):
+    _cuda_tensor(h, "h", torch.bfloat16)
+    _cuda_tensor(w, "w", torch.bfloat16)
+    if h.dim() != 2 or w.dim() != 2 or h.shape[1] != w.shape[1]:
+        raise ValueError("h must be [N, hidden] and w [V, hidden]")
+    N, hidden = h.shape
+    V = w.shape[0]
+    _cuda_tensor(labels, "labels", torch.int32)
+    if bias is not None:
+        _cuda_tensor(bias, "bias", torch.float32)
+    for name, t, n in (("w", w, None), ("labels", labels, N), ("bias", bias, V)):
+        if t is not None:
+            _same_place(t, name, h)
+            if n is not None and t.numel() != n:
+                raise ValueError(f"{name} must have {n} elements")
+    return N, hidden, V
+
+
+def _rows(t, name, N, h):
+    if t is None:
+        return torch.empty(N, dtype=torch.float32, device=h.device)
+    _cuda_tensor(t, name, torch.float32)
+    _same_place(t, name, h)
+    if t.numel() != N:
+        raise ValueError(f"{name} must have {N} elements")
+    return t
+
+
+def _ce_workspace(workspace, N, hidden, V, pass_, h):
+    if workspace is None:
+        return torch.empty(bb_linear_ce_workspace_size(N, hidden, V, pass_), dtype=torch.uint8,
+                           device=h.device)
+    _cuda_tensor(workspace, "workspace")
+    _same_place(workspace, "workspace", h)
+    return workspace
+
+
+def bb_linear_ce_fwd(h, w, bias, labels, loss=None, lse=None, workspace=None, stream=None):
+    """Softmax cross entropy of the vocabulary projection (see
+    include/bb_attn.h): h [N, hidden] and w [V, hidden] bf16, bias [V] fp32 or
+    None, labels [N] int32 (negative: no loss); returns loss, lse [N] fp32.
+    workspace: uint8 of bb_linear_ce_workspace_size(N, hidden, V, 0) bytes, or
+    None (allocated here; its status word is then out of reach)."""
+    N, hidden, V = _ce_tensors(h, w, bias, labels)
+    with _scope(h, stream):
+        loss, lse = _rows(loss, "loss", N, h), _rows(lse, "lse", N, h)
+        workspace = _ce_workspace(workspace, N, hidden, V, 0, h)
+        _check(lib().bb_linear_ce_fwd(N, hidden, V, _ptr(h), _ptr(w), _ptr(bias), _ptr(labels),
+                                      _ptr(loss), _ptr(lse), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(),
+                                      _stream_ptr(None)), "bb_linear_ce_fwd")
+    return loss, lse
+
+
+def bb_linear_ce_bwd(h, w, bias, labels, lse, dloss, dh=None, dw=None, dbias=None,
+                     workspace=None, stream=None):
+    """Gradients of bb_linear_ce_fwd for upstream dloss [N] fp32: returns dh
+    [N, hidden], dw [V, hidden] bf16 and dbias [V] fp32 (None where bias is
+    None and no dbias was given).  workspace: uint8 of
+    bb_linear_ce_workspace_size(N, hidden, V, 1) bytes, or None."""
+    N, hidden, V = _ce_tensors(h, w, bias, labels)
+    if lse is None or dloss is None:
+        raise ValueError("lse and dloss are needed")
+    with _scope(h, stream):
+        _rows(lse, "lse", N, h)
+        _rows(dloss, "dloss", N, h)
+        dh, dw = _like(dh, "dh", h), _like(dw, "dw", w)
+        if dbias is not None or bias is not None:
+            dbias = _rows(dbias, "dbias", V, h)
+        workspace = _ce_workspace(workspace, N, hidden, V, 1, h)
+        _check(lib().bb_linear_ce_bwd(N, hidden, V, _ptr(h), _ptr(w), _ptr(bias), _ptr(labels),
+                                      _ptr(lse), _ptr(dloss), _ptr(dh), _ptr(dw), _ptr(dbias),
+                                      _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(),
+                                      _stream_ptr(None)), "bb_linear_ce_bwd")
+    return dh, dw, dbias
 
 
 def bb_attn_noalloc_status(stream=None):

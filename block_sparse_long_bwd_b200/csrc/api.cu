@@ -163,6 +163,7 @@ const char* bb_status_str(int status) {
     case BB_ERR_WORKSPACE: return "workspace missing or too small";
     case BB_ERR_TIMEOUT: return "a device wait ran out of iterations";
     case BB_ERR_BAD_TABLE: return "random table entry out of range (ignored)";
+    case BB_ERR_BAD_LABEL: return "label outside the vocabulary (row ignored)";
     default: return "unknown status";
   }
 }

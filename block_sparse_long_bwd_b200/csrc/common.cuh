@@ -132,6 +132,9 @@ bool encode_tensor_maps(const Problem& p, int pass, TensorMaps* tm);
 // box box_inner x box_rows, 128-byte swizzle (box_inner = 64).
 bool encode_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
                     uint64_t row_stride, uint32_t box_inner, uint32_t box_rows);
+// The same for fp32 (row stride a multiple of 4, box_inner = 32).
+bool encode_f32_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
+                   uint64_t row_stride, uint32_t box_inner, uint32_t box_rows);
 
 // Tensor-core path (bf16, block 64, d 64).
 bool tc_fwd_supported(const Problem& p);

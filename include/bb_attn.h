@@ -62,8 +62,10 @@ typedef enum {
   BB_ERR_CUDA = -3,        /* a CUDA runtime call failed (launch, copy) */
   BB_ERR_WORKSPACE = -4,   /* workspace NULL or smaller than required */
   BB_ERR_TIMEOUT = -5,     /* (status word) a bounded device wait ran out */
-  BB_ERR_BAD_TABLE = -6    /* (status word) a random-table entry outside
+  BB_ERR_BAD_TABLE = -6,   /* (status word) a random-table entry outside
                               [-1, nb) was found and ignored */
+  BB_ERR_BAD_LABEL = -7    /* (status word) a label >= V was found; its row
+                              was treated as one without a label */
 } bb_status;
 
 typedef enum { BB_F32 = 0, BB_BF16 = 1 } bb_dtype;
@@ -343,6 +345,53 @@ BB_API int bb_qk_norm_rope_bwd(const bb_qk_desc* desc, const void* q, const void
                                const int32_t* positions, const void* dq_out, const void* dk_out,
                                void* dq, void* dk, float* dgamma_q, float* dgamma_k,
                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Softmax cross entropy of the vocabulary projection (the masked-language-
+ * model loss the pages' encoder is pretrained with, [ai-papers page] section
+ * "计算设置"), without the logits in memory, on tcgen05 tensor cores.  For N
+ * rows of `hidden` features and a vocabulary of V:
+ *   z[n][v] = bias[v] + sum_c h[n][c] w[v][c]
+ *   lse[n]  = log sum_v exp z[n][v],   loss[n] = lse[n] - z[n][labels[n]]
+ * A row whose label is negative has no loss: loss and lse are 0, and nothing
+ * of the row enters any result (its h may hold anything).  A label >= V is
+ * treated the same and flagged in the status word (BB_ERR_BAD_LABEL).  The
+ * cost follows the rows that have a label.  A bias of -infinity excludes its
+ * word.  bf16 products are summed in fp32; maxima, sums and logarithms are
+ * fp32.
+ *   h       [N][hidden] bf16, device
+ *   w       [V][hidden] bf16, device;  bias [V] fp32, device, or NULL
+ *   labels  [N] int32, device
+ *   loss, lse [N] fp32, device (written)
+ *   workspace device, >= bb_linear_ce_workspace_size(N, hidden, V, 0) bytes,
+ *             16-byte aligned; its status word is read by bb_attn_check_status
+ * Requires hidden % 8 == 0, 64 <= hidden <= 65536 and N, V <= 2^24, else
+ * BB_ERR_UNSUPPORTED; N, V >= 1. */
+BB_API int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w,
+                            const float* bias, const int32_t* labels, float* loss, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of bb_linear_ce_fwd for upstream dloss [N] (dloss[n] is read for
+ * rows with a label only; a mean over R labelled rows passes 1 / R):
+ *   dz[n][v] = dloss[n] (exp(z[n][v] - lse[n]) - [v = labels[n]])
+ *   dh[n][c] = sum_v dz[n][v] w[v][c]      (0 for rows without a label)
+ *   dw[v][c] = sum_n dz[n][v] h[n][c],   dbias[v] = sum_n dz[n][v]
+ * The logits are computed again, a piece of the vocabulary at a time: the
+ * workspace holds dz of one piece (at most 256 MiB, 512 columns at least),
+ * never of all.  dz is rounded to bf16 for the two products (dbias is summed
+ * before that rounding); sums are fp32 and dh, dw are rounded once.
+ *   lse      [N] fp32, device, as bb_linear_ce_fwd wrote it
+ *   dh       [N][hidden] bf16, device (written)
+ *   dw       [V][hidden] bf16, device (written)
+ *   dbias    [V] fp32, device (written), or NULL (not wanted)
+ *   workspace device, >= bb_linear_ce_workspace_size(N, hidden, V, 1) bytes */
+BB_API int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w,
+                            const float* bias, const int32_t* labels, const float* lse,
+                            const float* dloss, void* dh, void* dw, float* dbias,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace bb_linear_ce_fwd (pass 0) or bb_linear_ce_bwd
+ * (pass 1) needs; written to *bytes.  Host only. */
+BB_API int bb_linear_ce_workspace_size(int N, int hidden, int V, int pass, size_t* bytes);
 
 /* Number of kernel launches bb_attn_fwd (pass 0) or bb_attn_bwd (pass 1)
  * makes for `desc`, written to *launches.  Host only. */

@@ -76,3 +76,47 @@ def test_binding_refuses_host_tensors_and_wrong_types():
     q = torch.zeros((2, 3, 50, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         bb.bb_qk_norm_rope_fwd(_qk(), q, q, None, None)
+
+
+def test_linear_ce_refusals():
+    lib = bb.lib()
+    n = ctypes.c_size_t(0)
+    size = lib.bb_linear_ce_workspace_size
+    for args, code in (((0, 64, 10), -1), ((5, 0, 10), -1), ((5, 64, 0), -1), ((-1, 64, 10), -1),
+                       ((5, 60, 10), -2), ((5, 56, 10), -2), ((5, 65544, 10), -2),
+                       ((1 << 25, 64, 10), -2), ((5, 64, 1 << 25), -2),
+                       ((1 << 24, 64, 1 << 24), -2)):
+        assert size(*args, 0, ctypes.byref(n)) == code, args
+        assert lib.bb_linear_ce_fwd(*args, P, P, P, P, P, P, P, 1 << 40, None) == code
+        assert lib.bb_linear_ce_bwd(*args, P, P, P, P, P, P, P, P, P, P, 1 << 40, None) == code
+    assert size(5, 64, 10, 2, ctypes.byref(n)) == -1
+    assert size(5, 64, 10, 0, None) == -1
+    dims = (100, 128, 1000)
+    f, b = (bb.bb_linear_ce_workspace_size(*dims, p) for p in (0, 1))
+    good = [P] * 7
+    assert lib.bb_linear_ce_fwd(*dims, *good, f - 1, None) == -4
+    for i, code in ((0, -1), (1, -1), (3, -1), (4, -1), (5, -1), (6, -4)):
+        a = list(good)
+        a[i] = None
+        assert lib.bb_linear_ce_fwd(*dims, *a, f, None) == code, i
+        a[i] = P + 4
+        assert lib.bb_linear_ce_fwd(*dims, *a, f, None) == -1, i
+    good = [P] * 10
+    assert lib.bb_linear_ce_bwd(*dims, *good, b - 1, None) == -4
+    for i, code in ((0, -1), (1, -1), (3, -1), (4, -1), (5, -1), (6, -1), (7, -1), (9, -4)):
+        a = list(good)
+        a[i] = None
+        assert lib.bb_linear_ce_bwd(*dims, *a, b, None) == code, i
+        a[i] = P + 4
+        assert lib.bb_linear_ce_bwd(*dims, *a, b, None) == -1, i
+
+
+def test_linear_ce_workspace_is_bounded_by_a_piece():
+    """The backward's workspace holds one piece of the vocabulary (256 MiB of
+    dz at most), not the N x V logits."""
+    N, D, V = 32768, 1024, 200000
+    need = bb.bb_linear_ce_workspace_size(N, D, V, 1)
+    # dz of a piece, packed rows, fp32 dh, and the dbias sums of a piece
+    assert need < (256 << 20) + N * D * 2 + N * D * 4 + N // 128 * 8192 * 4 + (4 << 20)
+    assert need < N * V * 2 // 10
+    assert bb.bb_status_str(bb.BB_ERR_BAD_LABEL) != bb.bb_status_str(42)
