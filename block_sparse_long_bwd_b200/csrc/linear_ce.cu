@@ -35,15 +35,21 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;
-constexpr int kStages = 3;
+// A tile of the GEMMs is 256 x 256: a pair of CTAs (cta_group::2), 128 rows of
+// A and 128 columns of B in each one's shared memory, 128 x 256 accumulators
+// in each one's tensor memory, two of them, so that a tile's epilogue runs
+// under the next tile's MMAs.
+constexpr int kBM = 128;                            // rows of a CTA
+constexpr int kTM = 2 * kBM, kTN = 256, kBK = 64;   // tile of a pair, K step
+constexpr int kStages = 5;
 constexpr uint32_t kBox = 64 * 64 * 2;              // one 64 x 64 bf16 box: 8 KB
-constexpr uint32_t kATile = kBM * kBK * 2;          // 16 KB
-constexpr uint32_t kBTile = kBN * kBK * 2;          // 32 KB
-constexpr uint32_t kStageBytes = kATile + kBTile;   // 48 KB
-constexpr uint32_t kStageOut = 4 * 4 * 4096;        // 4 warps x 4 blocks x 32 x 128 B
-constexpr int kThreads = 192;
+constexpr uint32_t kOpTile = 128 * kBK * 2;         // a CTA's part of A or B: 16 KB
+constexpr uint32_t kStageBytes = 2 * kOpTile;       // 32 KB
+constexpr int kEpiWarps = 8;                        // two per TMEM lane quarter
+constexpr uint32_t kStageOut = kEpiWarps * 4096;    // a 32 x 128 B block per warp
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kTmemCols = 512;                 // two 128 x 256 fp32 accumulators
+constexpr int kHalf = kTN / 2;                      // columns of an epilogue warp
 constexpr size_t kPieceBytes = 256u << 20;          // dz of one vocabulary piece
 
 enum Mode { kLse = 0, kDz = 1, kGrad = 2 };
@@ -59,7 +65,7 @@ struct Info {
 
 struct CeArgs {
   int N, D, V;
-  int N128;          // N rounded up to 128
+  int Np;            // N rounded up to a tile's rows
   int Vp;            // columns of a piece (a multiple of 256)
   int v0, vn;        // this piece: first column, columns
   int splits;        // parts the piece's columns are cut into for dh
@@ -69,9 +75,9 @@ struct CeArgs {
   const int* lab;      // packed rows: label,
   const float* rlse;   //   lse,
   const float* dls;    //   dloss / dlref
-  float2* part;        // [vocabulary tiles][N128] (max, sum of exponentials)
+  float2* part;        // [vocabulary half tiles][Np] (max, sum of exponentials)
   float* zl;           // [N] logit of the label
-  float* dbp;          // [row tiles][Vp] column sums of dz, or null
+  float* dbp;          // [Np / 128][Vp] column sums of dz, or null
   float* dbias;        // [V], with dbp
 };
 
@@ -84,7 +90,7 @@ struct Job {
   int dw;           // kGrad: 1 = a tile of dW, 0 = of dh
   int m0, n0;       // first row and column of the tile
   int k0, ksteps;   // first K index, 64-wide K steps
-  int nblk;         // 64-column blocks of the tile
+  int nblk;         // 64-column blocks of B in each CTA: the tile has 128 nblk columns
   int row0;         // first row in the output
 };
 
@@ -92,13 +98,13 @@ template <int kMode>
 struct Work {
   int tiles, mt, dn, wm, th, hks, wks, dh_first;
   __device__ __forceinline__ Work(const CeArgs& a, int rows) {
-    mt = (rows + kBM - 1) / kBM;
+    mt = (rows + kTM - 1) / kTM;
     if (kMode != kGrad) {
-      tiles = mt * ((a.vn + kBN - 1) / kBN);
+      tiles = mt * ((a.vn + kTN - 1) / kTN);
       return;
     }
-    dn = (a.D + kBN - 1) / kBN;
-    wm = (a.vn + kBM - 1) / kBM;
+    dn = (a.D + kTN - 1) / kTN;
+    wm = (a.vn + kTM - 1) / kTM;
     hks = (a.vn + kBK - 1) / kBK;
     wks = (rows + kBK - 1) / kBK;
     th = mt * dn * a.splits;
@@ -108,12 +114,12 @@ struct Work {
   }
   __device__ __forceinline__ Job job(const CeArgs& a, int t) const {
     Job j;
-    j.nblk = kBN / 64;
+    j.nblk = 2;
     if (kMode != kGrad) {
       // Row tiles run fastest: the rows stay in L2 while W streams by once.
       j.dw = 0;
-      j.m0 = (t % mt) * kBM;
-      j.n0 = (t / mt) * kBN;
+      j.m0 = (t % mt) * kTM;
+      j.n0 = (t / mt) * kTN;
       j.k0 = 0;
       j.ksteps = (a.D + kBK - 1) / kBK;
       j.row0 = j.m0;
@@ -123,21 +129,20 @@ struct Work {
     int u = t;
     if (dh_first && j.dw) u -= th;
     if (!dh_first && !j.dw) u -= wm * dn;
-    j.n0 = (u % dn) * kBN;
-    const int left = (a.D - j.n0 + 63) / 64;
-    j.nblk = left < j.nblk ? left : j.nblk;
+    j.n0 = (u % dn) * kTN;
+    if (a.D - j.n0 <= 128) j.nblk = 1;
     u /= dn;
     if (j.dw) {
-      j.m0 = u * kBM;
+      j.m0 = u * kTM;
       j.k0 = 0;
       j.ksteps = wks;
       j.row0 = a.v0 + j.m0;
     } else {
       const int s = u / mt;
-      j.m0 = (u % mt) * kBM;
+      j.m0 = (u % mt) * kTM;
       j.k0 = (int)((long long)hks * s / a.splits);
       j.ksteps = (int)((long long)hks * (s + 1) / a.splits) - j.k0;
-      j.row0 = s * a.N128 + j.m0;
+      j.row0 = s * a.Np + j.m0;
     }
     return j;
   }
@@ -196,17 +201,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Bars bars;
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
-  __shared__ float red[2][4][kBN];  // kDz: column sums of each warp's 32 rows
+  __shared__ float red[2][4][kTN];  // kDz: column sums of each warp's 32 rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint8_t* stages = base;                              // [kStages][A | B]
-  uint8_t* stage_out = base + kStages * kStageBytes;   // [4 warps][4 blocks][32][128 B]
+  uint8_t* stage_out = base + kStages * kStageBytes;   // [8 warps][32][128 B]
   int* status = &a.info->status;
   const int rows = a.info->rows;
   const CUtensorMap* mapH = a.info->direct ? &tmH : &tmHp;
   const Work<kMode> work(a, rows);
 
+  // Barriers of the pair: `full` and `acc_empty` are used in rank 0 only (it
+  // issues the MMAs); both CTAs' loads and epilogue warps signal them there.
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < kStages; ++s) {
@@ -215,27 +224,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.acc_full[s], 1);
-      mbar_init(&bars.acc_empty[s], 4);
+      mbar_init(&bars.acc_empty[s], 2 * kEpiWarps);
     }
-    mbar_init(&bars.red, 4);
+    mbar_init(&bars.red, kEpiWarps);
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&tmem_base_sh, kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(&tmem_base_sh, kTmemCols);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
 
   if (warp == 0) {
-    // ---------------- TMA loads (one thread) ----------------
+    // ---------------- TMA loads (one thread of each CTA) ----------------
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < work.tiles && ok; t += gridDim.x) {
+      for (int t = pair; t < work.tiles && ok; t += pairs) {
         const Job j = work.job(a, t);
+        const int m0 = j.m0 + rank * kBM, n0 = j.n0 + rank * 64 * j.nblk;
         for (int ks = 0; ks < j.ksteps; ++ks, ++it) {
           const uint32_t st = it % kStages;
           if (!mbar_wait(&bars.empty[st], ((it / kStages) & 1) ^ 1, &abort_flag, status)) {
@@ -243,27 +254,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           uint8_t* pa = stages + st * kStageBytes;
-          uint8_t* pb = pa + kATile;
-          uint64_t* bar = &bars.full[st];
-          const int k = j.k0 + ks;
+          uint8_t* pb = pa + kOpTile;
+          const uint32_t bar = map_rank(&bars.full[st], 0);
+          if (rank == 0) mbar_expect_tx(&bars.full[st], 2 * (kOpTile + j.nblk * kBox));
+          const int k = (j.k0 + ks) * kBK;
           if (kMode != kGrad) {
-            mbar_expect_tx(bar, kStageBytes);
-            tma_load_2d(pa, mapH, bar, k * kBK, j.m0);
-            tma_load_2d(pb, &tmW, bar, k * kBK, a.v0 + j.n0);
+            tma_load_2d_pair(pa, mapH, bar, k, m0);
+            tma_load_2d_pair(pb, &tmW, bar, k, a.v0 + n0);
           } else {
-            mbar_expect_tx(bar, kATile + j.nblk * kBox);
             // dW: A = dz^T (columns of dz along M), B = h; dh: A = dz, B = W.
             for (int i = 0; i < 2; ++i)
-              tma_load_2d(pa + i * kBox, &tmDz, bar, j.dw ? j.m0 + 64 * i : k * kBK,
-                          j.dw ? k * kBK : j.m0 + 64 * i);
+              tma_load_2d_pair(pa + i * kBox, &tmDz, bar, j.dw ? m0 + 64 * i : k,
+                               j.dw ? k : m0 + 64 * i);
             for (int i = 0; i < j.nblk; ++i)
-              tma_load_2d(pb + i * kBox, j.dw ? mapH : &tmW, bar, j.n0 + 64 * i,
-                          j.dw ? k * kBK : a.v0 + k * kBK);
+              tma_load_2d_pair(pb + i * kBox, j.dw ? mapH : &tmW, bar, n0 + 64 * i,
+                               j.dw ? k : a.v0 + k);
           }
         }
       }
-      if (abort_flag) {
-        // Let issued copies land before shared memory goes away.
+      // The last stages' releases reach this CTA before it may leave.
+      for (int i = 0; i < kStages && ok; ++i, ++it)
+        ok = mbar_wait(&bars.empty[it % kStages], ((it / kStages) & 1) ^ 1, &abort_flag, status);
+      if (abort_flag && rank == 0) {
+        // Let issued copies (both CTAs') land before shared memory goes away;
+        // rank 1 waits at the cluster barrier meanwhile.
         for (uint32_t s = 0; s < (uint32_t)kStages; ++s)
           if (it >= s + 1) {
             const uint32_t last = it - 1 - ((it - 1 - s) % kStages);
@@ -275,17 +289,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ---------------- MMA issue (one thread) ----------------
+    // ---------------- MMA issue (one thread of rank 0) ----------------
     uint32_t it = 0, tc = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < work.tiles && ok; t += gridDim.x, ++tc) {
+    bool ok = rank == 0;
+    for (int t = pair; t < work.tiles && ok; t += pairs, ++tc) {
       const Job j = work.job(a, t);
       const int acc = tc & 1;
       if (!mbar_wait(&bars.acc_empty[acc], ((tc >> 1) & 1) ^ 1, &abort_flag, status)) break;
       tc_fence_after();
       // K-major tiles step 32 bytes per 16 of K; MN-major ones 16 rows of 128.
       const uint32_t a_mn = kMode == kGrad && j.dw, b_mn = kMode == kGrad;
-      const uint32_t idesc = idesc_bf16(kBM, 64 * j.nblk, a_mn, b_mn);
+      const uint32_t idesc = idesc_bf16(kTM, 128 * j.nblk, a_mn, b_mn);
       const uint32_t astep = a_mn ? 2048 : 32, bstep = b_mn ? 2048 : 32;
       const uint32_t albo = a_mn ? kBox : 16, blbo = b_mn ? kBox : 16;
       for (int ks = 0; ks < j.ksteps; ++ks, ++it) {
@@ -297,38 +311,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (lane == 0) {
           const uint32_t aaddr = smem_u32(stages + st * kStageBytes);
-          const uint32_t baddr = aaddr + kATile;
+          const uint32_t baddr = aaddr + kOpTile;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss(tmem + acc * kBN, sdesc_sw128(aaddr + kk * astep, albo),
-                   sdesc_sw128(baddr + kk * bstep, blbo), idesc, (ks > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&bars.empty[st]);
+            mma_ss_pair(tmem + acc * kTN, sdesc_sw128(aaddr + kk * astep, albo),
+                        sdesc_sw128(baddr + kk * bstep, blbo), idesc,
+                        (ks > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_pair(&bars.empty[st]);
         }
         __syncwarp();
       }
-      if (ok && lane == 0) mma_commit(&bars.acc_full[acc]);
+      if (ok && lane == 0) mma_commit_pair(&bars.acc_full[acc]);
       __syncwarp();
     }
   } else {
-    // ---------------- epilogue (warps 2-5, 32 rows each) ----------------
-    const int quarter = warp & 3;
+    // ------- epilogue (warps 2-9: 32 rows and half of the columns each) -------
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    uint8_t* stage = stage_out + quarter * 4 * 4096;
+    uint8_t* stage = stage_out + (warp - 2) * 4096;
+    uint8_t* rowp = stage + lane * 128;
     const int swz = lane & 7;
     const float dlref = kMode == kGrad ? a.info->dlref : 1.f;
+    const uint32_t acc_empty = map_rank(&bars.acc_empty[0], 0);
     uint32_t tc = 0;
-    for (int t = blockIdx.x; t < work.tiles; t += gridDim.x, ++tc) {
+    for (int t = pair; t < work.tiles; t += pairs, ++tc) {
       const Job j = work.job(a, t);
       const int acc = tc & 1;
       if (!mbar_wait(&bars.acc_full[acc], (tc >> 1) & 1, &abort_flag, status)) break;
       tc_fence_after();
-      const uint32_t tz = tmem + acc * kBN + lane_off;
-      const int row = j.m0 + quarter * 32 + lane;  // packed row (kLse, kDz)
+      const uint32_t tz = tmem + acc * kTN + lane_off;
+      const int r0 = rank * kBM + quarter * 32;  // this warp's first row in the tile
+      const int row = j.m0 + r0 + lane;          // packed row (kLse, kDz)
+      const int cbeg = half * kHalf;
       if (kMode == kLse) {
         const int lab = row < rows ? __ldg(a.lab + row) : -1;
         float m = -INFINITY, s = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < kBN; c += 32) {
+        for (int c = cbeg; c < cbeg + kHalf; c += 32) {
           const int c0 = j.n0 + c;
           if (c0 >= a.V) break;
           float z[32];
@@ -358,20 +377,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.acc_empty[acc]);
-        a.part[(size_t)(j.n0 / kBN) * a.N128 + row] = make_float2(m, s);
+        if (lane == 0) mbar_arrive_cluster(acc_empty + 8 * acc);
+        a.part[(size_t)((j.n0 + cbeg) / kHalf) * a.Np + row] = make_float2(m, s);
         continue;
       }
-      // The previous tile's stores have read this warp's staging area.
-      if (lane == 0) bulk_wait_read_all();
-      __syncwarp();
       if (kMode == kDz) {
         const bool live = row < rows;
         const int lab = live ? __ldg(a.lab + row) - a.v0 : -1;
         const float lse = live ? __ldg(a.rlse + row) : 0.f;
         const float dl = live ? __ldg(a.dls + row) : 0.f;
 #pragma unroll 1
-        for (int c = 0; c < kBN; c += 32) {
+        for (int c = cbeg; c < cbeg + kHalf; c += 32) {
           const int c0 = j.n0 + c;  // column in the piece
           float z[32];
           logits32(a, tz + c, a.v0 + c0, 0.f, z);
@@ -389,7 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) z[e] = live && e < last ? z[e] : 0.f;
           }
-          uint8_t* rowp = stage + (c >> 6) * 4096 + lane * 128;
+          if ((c & 32) == 0) {
+            // The previous block's store has read the staging area.
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+          }
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch)
             *reinterpret_cast<uint4*>(rowp + (((((c >> 5) & 1) * 4 + ch) ^ swz) << 4)) =
@@ -397,45 +417,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                            pack_bf16(z[8 * ch + 2], z[8 * ch + 3]),
                            pack_bf16(z[8 * ch + 4], z[8 * ch + 5]),
                            pack_bf16(z[8 * ch + 6], z[8 * ch + 7]));
+          if (c & 32) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tmDz, stage, j.n0 + c - 32, j.m0 + r0);
+              bulk_commit_group();
+            }
+          }
           if (a.dbp) red[acc][quarter][c + lane] = column_sums(z, lane);
         }
         tc_fence_before();
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars.acc_empty[acc]);
-          for (int cb = 0; cb < 4; ++cb)
-            tma_store_2d(&tmDz, stage + cb * 4096, j.n0 + cb * 64, j.m0 + quarter * 32);
-          bulk_commit_group();
-        }
+        if (lane == 0) mbar_arrive_cluster(acc_empty + 8 * acc);
         if (a.dbp) {
-          // Column sums of the tile: the four warps' sums in order.
+          // Column sums of the CTA's 128 rows: the four quarters' sums in order.
           if (lane == 0) mbar_arrive_release(&bars.red);
           if (!mbar_wait(&bars.red, tc & 1, &abort_flag, status)) break;
-          for (int c = quarter * 64 + lane; c < quarter * 64 + 64; c += 32)
-            a.dbp[(size_t)(j.m0 / kBM) * a.Vp + j.n0 + c] =
-                red[acc][0][c] + red[acc][1][c] + red[acc][2][c] + red[acc][3][c];
+          const int c = (warp - 2) * 32 + lane;
+          a.dbp[(size_t)(j.m0 / kBM + rank) * a.Vp + j.n0 + c] =
+              red[acc][0][c] + red[acc][1][c] + red[acc][2][c] + red[acc][3][c];
         }
         continue;
       }
       // kGrad.  The first column tile of dW also sums dbias of its words,
-      // over the row tiles in order.
-      if (j.dw && j.n0 == 0 && a.dbp) {
-        const int v = j.m0 + quarter * 32 + lane;
+      // over the blocks of 128 rows in order.
+      if (j.dw && j.n0 == 0 && a.dbp && half == 0) {
+        const int v = j.m0 + r0 + lane;
+        const int blocks = (rows + kBM - 1) / kBM;
         float s = 0.f;
-        for (int m = 0; m < work.mt; ++m) s += a.dbp[(size_t)m * a.Vp + v];
+        for (int m = 0; m < blocks; ++m) s += a.dbp[(size_t)m * a.Vp + v];
         if (a.v0 + v < a.V) a.dbias[a.v0 + v] = s * dlref;
       }
       // A tile without K steps (no rows) is zero.
       const float f = j.ksteps > 0 ? 1.f : 0.f;
 #pragma unroll 1
-      for (int cb = 0; cb < j.nblk; ++cb) {
+      for (int cb = half * j.nblk; cb < (half + 1) * j.nblk; ++cb) {
         uint32_t v0[32], v1[32];
         tmem_ld32(tz + cb * 64, v0);
         tmem_ld32(tz + cb * 64 + 32, v1);
         tmem_ld_wait();
+        const int y = j.row0 + r0, x = j.n0 + cb * 64;
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
         if (j.dw) {
-          uint8_t* rowp = stage + cb * 4096 + lane * 128;
 #pragma unroll
           for (int ch = 0; ch < 8; ++ch) {
             const uint32_t* src = ch < 4 ? v0 + 8 * ch : v1 + 8 * (ch - 4);
@@ -447,54 +472,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]),
                            pack_bf16(g[6], g[7]));
           }
-        } else {
-          // fp32: two 32-column boxes; four staging slots serve two blocks.
-          if (cb == 2) {
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
-          }
-          uint8_t* rowp = stage + (cb & 1) * 8192 + lane * 128;
-#pragma unroll
-          for (int ch = 0; ch < 8; ++ch) {
-            *reinterpret_cast<uint4*>(rowp + ((ch ^ swz) << 4)) =
-                make_uint4(v0[4 * ch], v0[4 * ch + 1], v0[4 * ch + 2], v0[4 * ch + 3]);
-            *reinterpret_cast<uint4*>(rowp + 4096 + ((ch ^ swz) << 4)) =
-                make_uint4(v1[4 * ch], v1[4 * ch + 1], v1[4 * ch + 2], v1[4 * ch + 3]);
-          }
-        }
-        if (cb == j.nblk - 1) {
-          tc_fence_before();
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.acc_empty[acc]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          const int r0 = j.row0 + quarter * 32, c0 = j.n0 + cb * 64;
           // Boxes that start past the tensor's end have nothing to write.
-          if (j.dw) {
-            if (r0 < a.V) tma_store_2d(&tmDw, stage + cb * 4096, c0, r0);
-          } else {
-            for (int i = 0; i < 2 && c0 + 32 * i < a.D; ++i) {
-              const uint8_t* src = stage + (cb & 1) * 8192 + i * 4096;
+          if (lane == 0 && y < a.V && x < a.D) {
+            tma_store_2d(&tmDw, stage, x, y);
+            bulk_commit_group();
+          }
+        } else {
+          // fp32: two boxes of 32 columns, one after the other.
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t* v = i ? v1 : v0;
+            if (i) {
+              if (lane == 0) bulk_wait_read_all();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch)
+              *reinterpret_cast<uint4*>(rowp + ((ch ^ swz) << 4)) =
+                  make_uint4(v[4 * ch], v[4 * ch + 1], v[4 * ch + 2], v[4 * ch + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && x + 32 * i < a.D) {
               if (a.add)
-                tma_reduce_add_2d(&tmDh, src, c0 + 32 * i, r0);
+                tma_reduce_add_2d(&tmDh, stage, x + 32 * i, y);
               else
-                tma_store_2d(&tmDh, src, c0 + 32 * i, r0);
+                tma_store_2d(&tmDh, stage, x + 32 * i, y);
+              bulk_commit_group();
             }
           }
-          bulk_commit_group();
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc_empty + 8 * acc);
     }
     if (kMode != kLse && lane == 0) bulk_wait_all();  // output stores complete
   }
 
+  // Neither CTA leaves while the other may still signal its barriers.
   tc_fence_before();
   __syncthreads();
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
@@ -610,10 +633,10 @@ __global__ void __launch_bounds__(kRowsPerBlock) rows_kernel(const RowsArgs a) {
   }
 }
 
-// Forward: merges the vocabulary tiles' (max, sum) of 32 rows in a fixed
+// Forward: merges the vocabulary half tiles' (max, sum) of 32 rows in a fixed
 // order: eight warps take every eighth tile, then their eight pairs.
 __global__ void __launch_bounds__(256)
-    lse_merge_kernel(const Info* info, const float2* part, int vt, int N128, const float* zl,
+    lse_merge_kernel(const Info* info, const float2* part, int vt, int Np, const float* zl,
                      const int* idx, float* loss, float* lse) {
   __shared__ float2 sh[8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -622,7 +645,7 @@ __global__ void __launch_bounds__(256)
   if ((int)blockIdx.x * 32 >= rows) return;
   float m = -INFINITY, s = 0.f;
   for (int i = warp; i < vt; i += 8) {
-    const float2 p = part[(size_t)i * N128 + row];
+    const float2 p = part[(size_t)i * Np + row];
     const float mm = fmaxf(m, p.x);
     const float ref = mm == -INFINITY ? 0.f : mm;
     s = s * ex2((m - ref) * kLog2e) + p.y * ex2((p.x - ref) * kLog2e);
@@ -646,7 +669,7 @@ __global__ void __launch_bounds__(256)
 // Backward's end: dh rows rounded from the fp32 sums (0 where there is no
 // label), eight columns per thread.
 __global__ void __launch_bounds__(256)
-    dh_round_kernel(const Info* info, int N, int D, int N128, int splits, const int* pos,
+    dh_round_kernel(const Info* info, int N, int D, int Np, int splits, const int* pos,
                     const float* acc, uint16_t* dh) {
   const int chunks = D / 8;
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
@@ -658,7 +681,7 @@ __global__ void __launch_bounds__(256)
   if (p >= 0) {
     const float dlref = info->dlref;
     for (int s = 0; s < splits; ++s) {
-      const float4* src = reinterpret_cast<const float4*>(acc + ((size_t)s * N128 + p) * D + c);
+      const float4* src = reinterpret_cast<const float4*>(acc + ((size_t)s * Np + p) * D + c);
       const float4 x = src[0], y = src[1];
       v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
       v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
@@ -674,7 +697,7 @@ __global__ void __launch_bounds__(256)
 // ---- host -------------------------------------------------------------------
 
 struct Plan {
-  int N128, pieces, Vp, splits, vt;
+  int Np, pieces, Vp, splits, vt;
   size_t idx, pos, lab, rlse, dls, hp, part, zl, dz, dh, dbp, total;  // byte offsets
 };
 
@@ -684,20 +707,20 @@ int make_plan(int N, int D, int V, int pass, Plan* p) {
   if (N <= 0 || D <= 0 || V <= 0 || (pass != 0 && pass != 1)) return BB_ERR_INVALID;
   if (D % 8 != 0 || D < 64 || D > 65536 || N > (1 << 24) || V > (1 << 24))
     return BB_ERR_UNSUPPORTED;
-  p->N128 = (int)up(N, 128);
-  p->vt = (V + kBN - 1) / kBN;
-  if ((long long)(p->N128 / kBM) * p->vt >= (1ll << 31)) return BB_ERR_UNSUPPORTED;
+  p->Np = (int)up(N, kTM);
+  p->vt = (V + kTN - 1) / kTN;
+  if ((long long)(p->Np / kTM) * p->vt >= (1ll << 31)) return BB_ERR_UNSUPPORTED;
   // Pieces of equal size whose dz fits kPieceBytes (512 columns at least).
-  size_t cols = kPieceBytes / 2 / p->N128 / kBN * kBN;
+  size_t cols = kPieceBytes / 2 / p->Np / kTN * kTN;
   cols = cols < 512 ? 512 : cols;
   p->pieces = (int)((V + cols - 1) / cols);
-  p->Vp = (int)up((V + p->pieces - 1) / p->pieces, kBN);
+  p->Vp = (int)up((V + p->pieces - 1) / p->pieces, kTN);
   p->pieces = (V + p->Vp - 1) / p->Vp;
   // dh has few tiles of a long K when there are few rows: cut K so that a
-  // tile takes no more than half of a CTA's share of the launch.
-  const long long dn = (D + kBN - 1) / kBN, mt = p->N128 / kBM;
+  // tile takes no more than half of a pair's share of the launch.
+  const long long dn = (D + kTN - 1) / kTN, mt = p->Np / kTM;
   const long long hks = p->Vp / kBK, wks = (N + kBK - 1) / kBK;
-  const long long share = (mt * dn * hks + (long long)(p->Vp / kBM) * dn * wks) / (2 * 148);
+  const long long share = (mt * dn * hks + (long long)(p->Vp / kTM) * dn * wks) / (2 * 74);
   const long long len = share < 8 ? 8 : share;
   long long s = (hks + len - 1) / len;
   p->splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
@@ -709,17 +732,17 @@ int make_plan(int N, int D, int V, int pass, Plan* p) {
   };
   p->idx = take((size_t)N * 4);
   p->lab = take((size_t)N * 4);
-  p->hp = take((size_t)p->N128 * D * 2);
+  p->hp = take((size_t)p->Np * D * 2);
   if (pass == 0) {
-    p->part = take((size_t)p->vt * p->N128 * 8);
+    p->part = take((size_t)2 * p->vt * p->Np * 8);
     p->zl = take((size_t)N * 4);
   } else {
     p->pos = take((size_t)N * 4);
     p->rlse = take((size_t)N * 4);
     p->dls = take((size_t)N * 4);
-    p->dz = take((size_t)p->N128 * p->Vp * 2);
-    p->dh = take((size_t)p->splits * p->N128 * D * 4);
-    p->dbp = take((size_t)(p->N128 / kBM) * p->Vp * 4);
+    p->dz = take((size_t)p->Np * p->Vp * 2);
+    p->dh = take((size_t)p->splits * p->Np * D * 4);
+    p->dbp = take((size_t)(p->Np / kBM) * p->Vp * 4);
   }
   p->total = off;
   return BB_OK;
@@ -733,8 +756,19 @@ cudaError_t launch_gemm(const CeArgs& a, int tiles, int sms, const CUtensorMap& 
   cudaError_t e = cudaFuncSetAttribute(ce_gemm_kernel<kMode>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  ce_gemm_kernel<kMode><<<tiles < sms ? tiles : sms, kThreads, smem, s>>>(a, h, hp, w, dz, dw, dh);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * (tiles < sms / 2 ? tiles : sms / 2));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ce_gemm_kernel<kMode>, a, h, hp, w, dz, dw, dh);
 }
 
 int sm_count() {
@@ -774,8 +808,8 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
   cudaStream_t s = (cudaStream_t)stream;
   CUtensorMap tmH, tmHp, tmW;
   if (!encode_bf16_2d(&tmH, h, hidden, N, hidden, 64, kBM) ||
-      !encode_bf16_2d(&tmHp, ws + p.hp, hidden, p.N128, hidden, 64, kBM) ||
-      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, kBN))
+      !encode_bf16_2d(&tmHp, ws + p.hp, hidden, p.Np, hidden, 64, kBM) ||
+      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, 128))
     return BB_ERR_CUDA;
   RowsArgs r{};
   r.N = N;
@@ -795,17 +829,17 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
   a.N = N;
   a.D = hidden;
   a.V = V;
-  a.N128 = p.N128;
+  a.Np = p.Np;
   a.vn = V;
   a.info = r.info;
   a.bias = bias;
   a.lab = r.lab;
   a.part = reinterpret_cast<float2*>(ws + p.part);
   a.zl = reinterpret_cast<float*>(ws + p.zl);
-  if (launch_gemm<kLse>(a, p.N128 / kBM * p.vt, sm_count(), tmH, tmHp, tmW, tmW, tmW, tmW, s) !=
+  if (launch_gemm<kLse>(a, p.Np / kTM * p.vt, sm_count(), tmH, tmHp, tmW, tmW, tmW, tmW, s) !=
       cudaSuccess)
     return BB_ERR_CUDA;
-  lse_merge_kernel<<<(N + 31) / 32, 256, 0, s>>>(a.info, a.part, p.vt, p.N128, a.zl, r.idx, loss,
+  lse_merge_kernel<<<(N + 31) / 32, 256, 0, s>>>(a.info, a.part, (V + kHalf - 1) / kHalf, p.Np, a.zl, r.idx, loss,
                                                  lse);
   return cudaGetLastError() == cudaSuccess ? BB_OK : BB_ERR_CUDA;
 }
@@ -826,15 +860,15 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   cudaStream_t s = (cudaStream_t)stream;
   CUtensorMap tmH, tmHp, tmW, tmH64, tmHp64, tmW64, tmDz32, tmDz64, tmDw, tmDh;
   if (!encode_bf16_2d(&tmH, h, hidden, N, hidden, 64, kBM) ||
-      !encode_bf16_2d(&tmHp, ws + p.hp, hidden, p.N128, hidden, 64, kBM) ||
-      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, kBN) ||
+      !encode_bf16_2d(&tmHp, ws + p.hp, hidden, p.Np, hidden, 64, kBM) ||
+      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, 128) ||
       !encode_bf16_2d(&tmH64, h, hidden, N, hidden, 64, 64) ||
-      !encode_bf16_2d(&tmHp64, ws + p.hp, hidden, p.N128, hidden, 64, 64) ||
+      !encode_bf16_2d(&tmHp64, ws + p.hp, hidden, p.Np, hidden, 64, 64) ||
       !encode_bf16_2d(&tmW64, w, hidden, V, hidden, 64, 64) ||
-      !encode_bf16_2d(&tmDz32, ws + p.dz, p.Vp, p.N128, p.Vp, 64, 32) ||
-      !encode_bf16_2d(&tmDz64, ws + p.dz, p.Vp, p.N128, p.Vp, 64, 64) ||
+      !encode_bf16_2d(&tmDz32, ws + p.dz, p.Vp, p.Np, p.Vp, 64, 32) ||
+      !encode_bf16_2d(&tmDz64, ws + p.dz, p.Vp, p.Np, p.Vp, 64, 64) ||
       !encode_bf16_2d(&tmDw, dw, hidden, V, hidden, 64, 32) ||
-      !encode_f32_2d(&tmDh, ws + p.dh, hidden, (uint64_t)p.splits * p.N128, hidden, 32, 32))
+      !encode_f32_2d(&tmDh, ws + p.dh, hidden, (uint64_t)p.splits * p.Np, hidden, 32, 32))
     return BB_ERR_CUDA;
   RowsArgs r{};
   r.N = N;
@@ -857,7 +891,7 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   a.N = N;
   a.D = hidden;
   a.V = V;
-  a.N128 = p.N128;
+  a.Np = p.Np;
   a.Vp = p.Vp;
   a.splits = p.splits;
   a.info = r.info;
@@ -867,19 +901,19 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   a.dls = r.dls;
   a.dbp = dbias ? reinterpret_cast<float*>(ws + p.dbp) : nullptr;
   a.dbias = dbias;
-  const int sms = sm_count(), mt = p.N128 / kBM, dn = (hidden + kBN - 1) / kBN;
+  const int sms = sm_count(), mt = p.Np / kTM, dn = (hidden + kTN - 1) / kTN;
   for (int i = 0; i < p.pieces; ++i) {
     a.v0 = i * p.Vp;
     a.vn = V - a.v0 < p.Vp ? V - a.v0 : p.Vp;
     a.add = i > 0;
-    const int nt = (a.vn + kBN - 1) / kBN, wm = (a.vn + kBM - 1) / kBM;
+    const int nt = (a.vn + kTN - 1) / kTN, wm = (a.vn + kTM - 1) / kTM;
     if (launch_gemm<kDz>(a, mt * nt, sms, tmH, tmHp, tmW, tmDz32, tmW, tmW, s) != cudaSuccess ||
         launch_gemm<kGrad>(a, mt * dn * p.splits + wm * dn, sms, tmH64, tmHp64, tmW64, tmDz64,
                            tmDw, tmDh, s) != cudaSuccess)
       return BB_ERR_CUDA;
   }
   dh_round_kernel<<<(unsigned)(((size_t)N * (hidden / 8) + 255) / 256), 256, 0, s>>>(
-      a.info, N, hidden, p.N128, p.splits, r.pos, reinterpret_cast<float*>(ws + p.dh),
+      a.info, N, hidden, p.Np, p.splits, r.pos, reinterpret_cast<float*>(ws + p.dh),
       static_cast<uint16_t*>(dh));
   return cudaGetLastError() == cudaSuccess ? BB_OK : BB_ERR_CUDA;
 }
