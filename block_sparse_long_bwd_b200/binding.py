@@ -368,77 +368,89 @@ def bb_out_proj(o, w_o, b_o, workspace, out=None, stream=None):
     return out
 
 
+_DTYPE_CODE = {torch.float32: BB_F32, torch.bfloat16: BB_BF16}
+
+
 def _dtype_code(t, name):
-    code = {torch.float32: BB_F32, torch.bfloat16: BB_BF16}.get(t.dtype)
+    code = _DTYPE_CODE.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be torch.float32 or torch.bfloat16")
     return code
 
 
-def _like(t, name, ref, dtype=None):
-    """t, or a new tensor where it is None, shaped like ref (dtype: ref's
-    unless given)."""
-    dtype = ref.dtype if dtype is None else dtype
+def _dense(t, name, dtype, device, shape=None):
+    """Checks of one argument: contiguous, on CUDA device number `device`, of
+    the dtype and (where given) shape."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+
+
+def _like(t, name, ref):
+    """t, or a new tensor where it is None, of ref's shape, dtype and device."""
     if t is None:
-        return torch.empty_like(ref, dtype=dtype)
-    _cuda_tensor(t, name, dtype)
-    _same_place(t, name, ref)
-    if t.shape != ref.shape:
-        raise ValueError(f"{name} must have shape {tuple(ref.shape)}")
+        return torch.empty_like(ref)
+    _dense(t, name, ref.dtype, ref.get_device(), ref.shape)
     return t
 
 
-def _same_place(t, name, ref):
-    if t.device != ref.device:
-        raise ValueError(f"{name} must be on {ref.device}")
-
-
-def _scope(ref, stream):
-    """Context of a call on ref's device and the given stream (None: that
-    device's current one), so that what the call allocates belongs to the
-    stream it runs on."""
+def _scope(device, stream):
+    """Context of a call on CUDA device number `device` and the given stream
+    (None: that device's current one), so that what the call allocates
+    belongs to the stream it runs on."""
     if stream is not None:
-        if stream.device != ref.device:
-            raise ValueError(f"stream must be on {ref.device}")
+        if stream.device.index != device:
+            raise ValueError(f"stream must be on cuda:{device}")
         return torch.cuda.stream(stream)
-    if ref.device.index != torch.cuda.current_device():
-        return torch.cuda.device(ref.device)
+    if device != torch.cuda.current_device():
+        return torch.cuda.device(device)
     return contextlib.nullcontext()
+
+
+def _current_stream_ptr(device):
+    """The device's current stream as a raw handle (a Stream object costs
+    microseconds, as much as a small launch)."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def bb_dropout_fwd(x, residual, rate, seed, site=0, out=None, stream=None):
     """Output dropout with the residual added (see include/bb_attn.h):
     x [...] bf16 or fp32, residual like x or None; returns out like x (out may
     be x or residual)."""
-    _cuda_tensor(x, "x")
-    code = _dtype_code(x, "x")
+    code, device = _dtype_code(x, "x"), x.get_device()
+    _dense(x, "x", x.dtype, device)
     if residual is not None:
-        _like(residual, "residual", x)
-    with _scope(x, stream):
+        _dense(residual, "residual", x.dtype, device, x.shape)
+    with _scope(device, stream):
         out = _like(out, "out", x)
-        _check(lib().bb_dropout_fwd(x.numel(), code, rate, seed & ((1 << 64) - 1), site, _ptr(x),
-                                    _ptr(residual), _ptr(out), _stream_ptr(None)),
-               "bb_dropout_fwd")
+        _check(lib().bb_dropout_fwd(x.numel(), code, rate, seed & ((1 << 64) - 1), site,
+                                    x.data_ptr(), _ptr(residual), out.data_ptr(),
+                                    _current_stream_ptr(device)), "bb_dropout_fwd")
     return out
 
 
 def bb_dropout_bwd(dout, rate, seed, site=0, dx=None, stream=None):
     """Gradient of bb_dropout_fwd's x (its residual's is dout); dx may be
     dout."""
-    _cuda_tensor(dout, "dout")
-    code = _dtype_code(dout, "dout")
-    with _scope(dout, stream):
+    code, device = _dtype_code(dout, "dout"), dout.get_device()
+    _dense(dout, "dout", dout.dtype, device)
+    with _scope(device, stream):
         dx = _like(dx, "dx", dout)
         _check(lib().bb_dropout_bwd(dout.numel(), code, rate, seed & ((1 << 64) - 1), site,
-                                    _ptr(dout), _ptr(dx), _stream_ptr(None)),
-               "bb_dropout_bwd")
+                                    dout.data_ptr(), dx.data_ptr(),
+                                    _current_stream_ptr(device)), "bb_dropout_bwd")
     return dx
 
 
 def make_qk_desc(B, H, L, dtype, eps=1e-6, theta=10000.0, rot_dim=64, interleaved=False, d=64):
     """Descriptor of bb_qk_norm_rope_fwd / _bwd (see include/bb_attn.h)."""
     if isinstance(dtype, torch.dtype):
-        dtype = {torch.float32: BB_F32, torch.bfloat16: BB_BF16}[dtype]
+        dtype = _DTYPE_CODE[dtype]
     return bb_qk_desc(B, H, L, d, dtype, eps, theta, rot_dim, int(interleaved))
 
 
@@ -449,27 +461,20 @@ def bb_qk_norm_rope_workspace_size(desc):
     return n.value
 
 
-def _qk_tensors(desc, tensors, gammas, positions):
-    """Checks of the tensors both passes read; tensors[0] sets the device."""
+def _qk_tensors(desc, tensors, gamma_q, gamma_k, positions):
+    """Checks of the tensors both passes read; returns their device number."""
     shape = (desc.B, desc.H, desc.L, desc.d)
     dtype = torch.float32 if desc.dtype == BB_F32 else torch.bfloat16
-    ref = tensors[0][1]
+    device = tensors[0][1].get_device()
     for name, t in tensors:
-        _cuda_tensor(t, name, dtype)
-        _same_place(t, name, ref)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}")
-    for name, t in gammas:
-        if t is not None:
-            _cuda_tensor(t, name, torch.float32)
-            _same_place(t, name, ref)
-            if t.numel() != desc.d:
-                raise ValueError(f"{name} must have {desc.d} elements")
+        _dense(t, name, dtype, device, shape)
+    if gamma_q is not None:
+        _dense(gamma_q, "gamma_q", torch.float32, device, (desc.d,))
+    if gamma_k is not None:
+        _dense(gamma_k, "gamma_k", torch.float32, device, (desc.d,))
     if positions is not None:
-        _cuda_tensor(positions, "positions", torch.int32)
-        _same_place(positions, "positions", ref)
-        if tuple(positions.shape) != (desc.B, desc.L):
-            raise ValueError(f"positions must have shape {(desc.B, desc.L)}")
+        _dense(positions, "positions", torch.int32, device, (desc.B, desc.L))
+    return device
 
 
 def bb_qk_norm_rope_fwd(desc, q, k, gamma_q, gamma_k, positions=None, q_out=None, k_out=None,
@@ -477,13 +482,13 @@ def bb_qk_norm_rope_fwd(desc, q, k, gamma_q, gamma_k, positions=None, q_out=None
     """Per-head RMS norm and rotary rotation of q and k [B, H, L, 64] (see
     include/bb_attn.h); gammas fp32 [64] or None, positions int32 [B, L] or
     None; returns q_out, k_out (which may be q, k)."""
-    _qk_tensors(desc, (("q", q), ("k", k)), (("gamma_q", gamma_q), ("gamma_k", gamma_k)),
-                positions)
-    with _scope(q, stream):
+    device = _qk_tensors(desc, (("q", q), ("k", k)), gamma_q, gamma_k, positions)
+    with _scope(device, stream):
         q_out, k_out = _like(q_out, "q_out", q), _like(k_out, "k_out", k)
         _check(lib().bb_qk_norm_rope_fwd(
-            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), _ptr(positions),
-            _ptr(q_out), _ptr(k_out), _stream_ptr(None)), "bb_qk_norm_rope_fwd")
+            ctypes.byref(desc), q.data_ptr(), k.data_ptr(), _ptr(gamma_q), _ptr(gamma_k),
+            _ptr(positions), q_out.data_ptr(), k_out.data_ptr(), _current_stream_ptr(device)),
+            "bb_qk_norm_rope_fwd")
     return q_out, k_out
 
 
@@ -493,21 +498,21 @@ def bb_qk_norm_rope_bwd(desc, q, k, gamma_q, gamma_k, positions, dq_out, dk_out,
     dq_out, dk_out: returns dq, dk (which may be dq_out, dk_out) and dgamma_q,
     dgamma_k fp32 [64].  workspace: uint8 of bb_qk_norm_rope_workspace_size
     bytes, or None (allocated here)."""
-    _qk_tensors(desc, (("q", q), ("k", k), ("dq_out", dq_out), ("dk_out", dk_out)),
-                (("gamma_q", gamma_q), ("gamma_k", gamma_k)), positions)
-    with _scope(q, stream):
+    device = _qk_tensors(desc, (("q", q), ("k", k), ("dq_out", dq_out), ("dk_out", dk_out)),
+                         gamma_q, gamma_k, positions)
+    with _scope(device, stream):
         dq, dk = _like(dq, "dq", q), _like(dk, "dk", k)
         dgamma = torch.empty((2, desc.d), dtype=torch.float32, device=q.device)
         if workspace is None:
             workspace = torch.empty(bb_qk_norm_rope_workspace_size(desc), dtype=torch.uint8,
                                     device=q.device)
-        _cuda_tensor(workspace, "workspace")
-        _same_place(workspace, "workspace", q)
+        _dense(workspace, "workspace", workspace.dtype, device)
         _check(lib().bb_qk_norm_rope_bwd(
-            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), _ptr(positions),
-            _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dgamma[0]), _ptr(dgamma[1]),
-            _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _stream_ptr(None)), "bb_qk_norm_rope_bwd")
+            ctypes.byref(desc), q.data_ptr(), k.data_ptr(), _ptr(gamma_q), _ptr(gamma_k),
+            _ptr(positions), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+            dgamma.data_ptr(), dgamma.data_ptr() + 4 * desc.d, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _current_stream_ptr(device)),
+            "bb_qk_norm_rope_bwd")
     return dq, dk, dgamma[0], dgamma[1]
 
 
@@ -519,30 +524,26 @@ def bb_linear_ce_workspace_size(N, hidden, V, pass_):
 
 
 def _ce_tensors(h, w, bias, labels):
-    _cuda_tensor(h, "h", torch.bfloat16)
-    _cuda_tensor(w, "w", torch.bfloat16)
+    """Checks of the tensors both passes read; returns N, hidden, V and their
+    device number."""
+    device = h.get_device()
+    _dense(h, "h", torch.bfloat16, device)
+    _dense(w, "w", torch.bfloat16, device)
     if h.dim() != 2 or w.dim() != 2 or h.shape[1] != w.shape[1]:
         raise ValueError("h must be [N, hidden] and w [V, hidden]")
     N, hidden = h.shape
     V = w.shape[0]
-    _cuda_tensor(labels, "labels", torch.int32)
+    _dense(labels, "labels", torch.int32, device, (N,))
     if bias is not None:
-        _cuda_tensor(bias, "bias", torch.float32)
-    for name, t, n in (("w", w, None), ("labels", labels, N), ("bias", bias, V)):
-        if t is not None:
-            _same_place(t, name, h)
-            if n is not None and t.numel() != n:
-                raise ValueError(f"{name} must have {n} elements")
-    return N, hidden, V
+        _dense(bias, "bias", torch.float32, device, (V,))
+    return N, hidden, V, device
 
 
-def _rows(t, name, N, h):
+def _fp32(t, name, n, h):
+    """t, or a new tensor where it is None: fp32 [n] on h's device."""
     if t is None:
-        return torch.empty(N, dtype=torch.float32, device=h.device)
-    _cuda_tensor(t, name, torch.float32)
-    _same_place(t, name, h)
-    if t.numel() != N:
-        raise ValueError(f"{name} must have {N} elements")
+        return torch.empty(n, dtype=torch.float32, device=h.device)
+    _dense(t, name, torch.float32, h.get_device(), (n,))
     return t
 
 
@@ -550,8 +551,7 @@ def _ce_workspace(workspace, N, hidden, V, pass_, h):
     if workspace is None:
         return torch.empty(bb_linear_ce_workspace_size(N, hidden, V, pass_), dtype=torch.uint8,
                            device=h.device)
-    _cuda_tensor(workspace, "workspace")
-    _same_place(workspace, "workspace", h)
+    _dense(workspace, "workspace", workspace.dtype, h.get_device())
     return workspace
 
 
@@ -561,14 +561,15 @@ def bb_linear_ce_fwd(h, w, bias, labels, loss=None, lse=None, workspace=None, st
     None, labels [N] int32 (negative: no loss); returns loss, lse [N] fp32.
     workspace: uint8 of bb_linear_ce_workspace_size(N, hidden, V, 0) bytes, or
     None (allocated here; its status word is then out of reach)."""
-    N, hidden, V = _ce_tensors(h, w, bias, labels)
-    with _scope(h, stream):
-        loss, lse = _rows(loss, "loss", N, h), _rows(lse, "lse", N, h)
+    N, hidden, V, device = _ce_tensors(h, w, bias, labels)
+    with _scope(device, stream):
+        loss, lse = _fp32(loss, "loss", N, h), _fp32(lse, "lse", N, h)
         workspace = _ce_workspace(workspace, N, hidden, V, 0, h)
-        _check(lib().bb_linear_ce_fwd(N, hidden, V, _ptr(h), _ptr(w), _ptr(bias), _ptr(labels),
-                                      _ptr(loss), _ptr(lse), _ptr(workspace),
+        _check(lib().bb_linear_ce_fwd(N, hidden, V, h.data_ptr(), w.data_ptr(), _ptr(bias),
+                                      labels.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                                      workspace.data_ptr(),
                                       workspace.numel() * workspace.element_size(),
-                                      _stream_ptr(None)), "bb_linear_ce_fwd")
+                                      _current_stream_ptr(device)), "bb_linear_ce_fwd")
     return loss, lse
 
 
@@ -578,21 +579,20 @@ def bb_linear_ce_bwd(h, w, bias, labels, lse, dloss, dh=None, dw=None, dbias=Non
     [N, hidden], dw [V, hidden] bf16 and dbias [V] fp32 (None where bias is
     None and no dbias was given).  workspace: uint8 of
     bb_linear_ce_workspace_size(N, hidden, V, 1) bytes, or None."""
-    N, hidden, V = _ce_tensors(h, w, bias, labels)
-    if lse is None or dloss is None:
-        raise ValueError("lse and dloss are needed")
-    with _scope(h, stream):
-        _rows(lse, "lse", N, h)
-        _rows(dloss, "dloss", N, h)
+    N, hidden, V, device = _ce_tensors(h, w, bias, labels)
+    _dense(lse, "lse", torch.float32, device, (N,))
+    _dense(dloss, "dloss", torch.float32, device, (N,))
+    with _scope(device, stream):
         dh, dw = _like(dh, "dh", h), _like(dw, "dw", w)
         if dbias is not None or bias is not None:
-            dbias = _rows(dbias, "dbias", V, h)
+            dbias = _fp32(dbias, "dbias", V, h)
         workspace = _ce_workspace(workspace, N, hidden, V, 1, h)
-        _check(lib().bb_linear_ce_bwd(N, hidden, V, _ptr(h), _ptr(w), _ptr(bias), _ptr(labels),
-                                      _ptr(lse), _ptr(dloss), _ptr(dh), _ptr(dw), _ptr(dbias),
-                                      _ptr(workspace),
+        _check(lib().bb_linear_ce_bwd(N, hidden, V, h.data_ptr(), w.data_ptr(), _ptr(bias),
+                                      labels.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
+                                      dh.data_ptr(), dw.data_ptr(), _ptr(dbias),
+                                      workspace.data_ptr(),
                                       workspace.numel() * workspace.element_size(),
-                                      _stream_ptr(None)), "bb_linear_ce_bwd")
+                                      _current_stream_ptr(device)), "bb_linear_ce_bwd")
     return dh, dw, dbias
 
 

@@ -12,13 +12,12 @@
 //   g = R^T dy,  dgamma = sum over rows of g n,  v = gamma g,
 //   dx = r (v - n mean(v n))
 //
-// Eight lanes own a row (eight components each); a warp takes four
-// consecutive tokens of one head, 512 (bf16) or 1024 (fp32) contiguous
-// bytes.  cos, sin and gamma of a lane's components depend on the token and
-// not on the head, so a lane computes them once, folds gamma into them and
-// walks its heads.  A component's partner sits eight components or a
-// multiple away (shuffle), beside it (interleaved pairs), or, for the other
-// rot_dim, is read again from L1.
+// Eight lanes own a row, four pairs each (both components of a pair, so the
+// rotation needs no other lane); a warp takes four consecutive tokens of one
+// head, 512 (bf16) or 1024 (fp32) contiguous bytes.  cos, sin and gamma of a
+// lane's pairs depend on the token and not on the head, so a lane computes
+// them once, folds gamma into them and walks its heads.  The 32 - rot_dim / 2
+// "pairs" behind the rotated ones are neighbouring components at angle 0.
 //
 // Angles: theta^(-2i / rot_dim) / 2 pi, a fraction of a turn per position, is
 // held as a 64-bit fixed-point number, so the product with the position
@@ -27,14 +26,21 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace bb {
 namespace {
 
+using namespace sm100;
+
 constexpr int kQkThreads = 256;
 constexpr int kTokensPerBlock = kQkThreads / 8;
-// Where a lane's partner components come from.
-enum PairMode { kShuffle = 0, kInterleaved = 1, kReload = 2 };
+// Where a lane finds its pairs' components.
+enum PairMode {
+  kHalves = 0,       // (i, i + half), half a multiple of 4: two runs of four
+  kInterleaved = 1,  // (2i, 2i + 1): one run of eight
+  kScattered = 2     // (i, i + half), any half: one by one
+};
 
 struct QkArgs {
   const void* in[2];        // q, k
@@ -50,59 +56,137 @@ struct QkArgs {
   uint64_t turn[32];        // turns per position of pair i, 64-bit fixed point
 };
 
-template <typename T>
-struct Row8;  // eight components of a row in registers
-template <>
-struct Row8<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    u = *reinterpret_cast<const uint4*>(p);
+// Components of pair p of a row (kHalves, from the lane's first pair on: the
+// runs of four keep their order within an unrotated lane).
+template <int kMode>
+__device__ __forceinline__ int comp_a(const QkArgs& a, int p) {
+  if (kMode == kInterleaved) return 2 * p;
+  if (p < a.half) return p;
+  if (kMode == kHalves) return a.rot + 2 * ((p & ~3) - a.half) + (p & 3);
+  return a.rot + 2 * (p - a.half);
+}
+template <int kMode>
+__device__ __forceinline__ int comp_b(const QkArgs& a, int p) {
+  if (kMode == kInterleaved) return 2 * p + 1;
+  if (p < a.half) return p + a.half;
+  return comp_a<kMode>(a, p) + (kMode == kHalves ? 4 : 1);
+}
+
+// Four pairs of a row in registers: a[e], b[e] the components of pair e.
+struct Pairs {
+  float2 a[2], b[2];
+};
+
+// A lane's part of a row as it lies in memory.
+template <typename T, int kMode>
+struct Raw;
+template <int kMode>
+struct Raw<__nv_bfloat16, kMode> {
+  uint32_t w[4];
+  static __device__ __forceinline__ float2 lohi(uint32_t x) {
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  __device__ __forceinline__ void load(const QkArgs& q, const __nv_bfloat16* row, int p, int oa,
+                                       int ob) {
+    if (kMode == kHalves) {
+      const uint2 x = *reinterpret_cast<const uint2*>(row + oa);
+      const uint2 y = *reinterpret_cast<const uint2*>(row + ob);
+      w[0] = x.x; w[1] = x.y; w[2] = y.x; w[3] = y.y;
+    } else if (kMode == kInterleaved) {
+      const uint4 x = *reinterpret_cast<const uint4*>(row + oa);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else {
+      const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      for (int e = 0; e < 4; ++e)
+        w[e] = r[comp_a<kMode>(q, p + e)] | ((uint32_t)r[comp_b<kMode>(q, p + e)] << 16);
     }
   }
-  __device__ __forceinline__ Row8 shfl(int src) const {
-    Row8 o;
-    o.u.x = __shfl_sync(0xffffffffu, u.x, src);
-    o.u.y = __shfl_sync(0xffffffffu, u.y, src);
-    o.u.z = __shfl_sync(0xffffffffu, u.z, src);
-    o.u.w = __shfl_sync(0xffffffffu, u.w, src);
+  __device__ __forceinline__ Pairs get() const {
+    Pairs o;
+    if (kMode == kHalves) {
+      o.a[0] = lohi(w[0]); o.a[1] = lohi(w[1]);
+      o.b[0] = lohi(w[2]); o.b[1] = lohi(w[3]);
+    } else {
+      const float2 x[4] = {lohi(w[0]), lohi(w[1]), lohi(w[2]), lohi(w[3])};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        o.a[i] = make_float2(x[2 * i].x, x[2 * i + 1].x);
+        o.b[i] = make_float2(x[2 * i].y, x[2 * i + 1].y);
+      }
+    }
     return o;
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
-    __nv_bfloat162 h[4];
+  static __device__ __forceinline__ void store(const QkArgs& q, __nv_bfloat16* row, int p, int oa,
+                                               int ob, const Pairs& v) {
+    if (kMode == kHalves) {
+      *reinterpret_cast<uint2*>(row + oa) =
+          make_uint2(pack(v.a[0].x, v.a[0].y), pack(v.a[1].x, v.a[1].y));
+      *reinterpret_cast<uint2*>(row + ob) =
+          make_uint2(pack(v.b[0].x, v.b[0].y), pack(v.b[1].x, v.b[1].y));
+    } else if (kMode == kInterleaved) {
+      *reinterpret_cast<uint4*>(row + oa) =
+          make_uint4(pack(v.a[0].x, v.b[0].x), pack(v.a[0].y, v.b[0].y),
+                     pack(v.a[1].x, v.b[1].x), pack(v.a[1].y, v.b[1].y));
+    } else {
+      const float x[4] = {v.a[0].x, v.a[0].y, v.a[1].x, v.a[1].y};
+      const float y[4] = {v.b[0].x, v.b[0].y, v.b[1].x, v.b[1].y};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+      for (int e = 0; e < 4; ++e) {
+        row[comp_a<kMode>(q, p + e)] = __float2bfloat16_rn(x[e]);
+        row[comp_b<kMode>(q, p + e)] = __float2bfloat16_rn(y[e]);
+      }
+    }
   }
 };
-template <>
-struct Row8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+template <int kMode>
+struct Raw<float, kMode> {
+  float4 x, y;
+  __device__ __forceinline__ void load(const QkArgs& q, const float* row, int p, int oa, int ob) {
+    if (kMode != kScattered) {
+      x = *reinterpret_cast<const float4*>(row + oa);
+      y = *reinterpret_cast<const float4*>(row + ob);
+    } else {
+      x = make_float4(row[comp_a<kMode>(q, p)], row[comp_a<kMode>(q, p + 1)],
+                      row[comp_a<kMode>(q, p + 2)], row[comp_a<kMode>(q, p + 3)]);
+      y = make_float4(row[comp_b<kMode>(q, p)], row[comp_b<kMode>(q, p + 1)],
+                      row[comp_b<kMode>(q, p + 2)], row[comp_b<kMode>(q, p + 3)]);
+    }
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-  __device__ __forceinline__ Row8 shfl(int src) const {
-    Row8 o;
-    o.a = make_float4(__shfl_sync(0xffffffffu, a.x, src), __shfl_sync(0xffffffffu, a.y, src),
-                      __shfl_sync(0xffffffffu, a.z, src), __shfl_sync(0xffffffffu, a.w, src));
-    o.b = make_float4(__shfl_sync(0xffffffffu, b.x, src), __shfl_sync(0xffffffffu, b.y, src),
-                      __shfl_sync(0xffffffffu, b.z, src), __shfl_sync(0xffffffffu, b.w, src));
+  __device__ __forceinline__ Pairs get() const {
+    Pairs o;
+    if (kMode == kInterleaved) {
+      o.a[0] = make_float2(x.x, x.z); o.a[1] = make_float2(y.x, y.z);
+      o.b[0] = make_float2(x.y, x.w); o.b[1] = make_float2(y.y, y.w);
+    } else {
+      o.a[0] = make_float2(x.x, x.y); o.a[1] = make_float2(x.z, x.w);
+      o.b[0] = make_float2(y.x, y.y); o.b[1] = make_float2(y.z, y.w);
+    }
     return o;
   }
-  static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  static __device__ __forceinline__ void store(const QkArgs& q, float* row, int p, int oa, int ob,
+                                               const Pairs& v) {
+    if (kMode == kInterleaved) {
+      *reinterpret_cast<float4*>(row + oa) =
+          make_float4(v.a[0].x, v.b[0].x, v.a[0].y, v.b[0].y);
+      *reinterpret_cast<float4*>(row + ob) =
+          make_float4(v.a[1].x, v.b[1].x, v.a[1].y, v.b[1].y);
+    } else if (kMode == kHalves) {
+      *reinterpret_cast<float4*>(row + oa) = make_float4(v.a[0].x, v.a[0].y, v.a[1].x, v.a[1].y);
+      *reinterpret_cast<float4*>(row + ob) = make_float4(v.b[0].x, v.b[0].y, v.b[1].x, v.b[1].y);
+    } else {
+      const float s[4] = {v.a[0].x, v.a[0].y, v.a[1].x, v.a[1].y};
+      const float t[4] = {v.b[0].x, v.b[0].y, v.b[1].x, v.b[1].y};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        row[comp_a<kMode>(q, p + e)] = s[e];
+        row[comp_b<kMode>(q, p + e)] = t[e];
+      }
+    }
   }
 };
 
@@ -114,55 +198,37 @@ __device__ __forceinline__ float sum8(float x) {
   return x;
 }
 
-// Index of the partner of component j, or j itself when it is not rotated.
-template <int kMode>
-__device__ __forceinline__ int partner_of(const QkArgs& a, int j) {
-  if (j >= a.rot) return j;
-  if (kMode == kInterleaved) return j ^ 1;
-  return j < a.half ? j + a.half : j - a.half;
-}
+__device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// The partners' values of a lane's eight components, given its own.
-template <typename T, int kMode>
-__device__ __forceinline__ void partners(const QkArgs& a, const Row8<T>& own,
-                                         const float (&v)[8], const T* row, int c0, int src,
-                                         float (&p)[8]) {
-  if (kMode == kShuffle) {
-    own.shfl(src).get(p);
-  } else if (kMode == kInterleaved) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = v[e ^ 1];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = to_f(row[partner_of<kMode>(a, c0 + e)]);
-  }
-  // An unrotated component has no partner (its sine is 0, but 0 times an
-  // infinity is not).
-  if (a.rot < kHeadDim) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = c0 + e < a.rot ? p[e] : 0.f;
-  }
-}
-
+// A lane reads its own components of a row before it writes them and no other
+// lane touches them, so the outputs may be the inputs.
 template <typename T, int kMode, bool kBwd>
-__global__ void __launch_bounds__(kQkThreads) qk_rope_kernel(const __grid_constant__ QkArgs a) {
+__global__ void __launch_bounds__(kQkThreads, kBwd ? 3 : 4)
+    qk_rope_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int kAhead = kBwd || sizeof(T) == 4 ? 2 : 4;
   __shared__ float red[kQkThreads / 32][64];
-  const int lane = threadIdx.x & 31, sub = lane & 7, c0 = sub * 8;
+  const int lane = threadIdx.x & 31, p0 = (lane & 7) * 4;
   const int t = blockIdx.y / a.hsplit;         // 0: q, 1: k
   const int split = blockIdx.y % a.hsplit;
   const int h0 = (int)((long long)a.H * split / a.hsplit);
   const int h1 = (int)((long long)a.H * (split + 1) / a.hsplit);
   const long long tokens = (long long)a.B * a.L;
-  // Lane that holds the partners (whole lanes swap when half is a multiple
-  // of eight).
-  const int hl = a.half >> 3;
-  const int src = kMode != kShuffle || c0 >= a.rot ? lane : (sub < hl ? lane + hl : lane - hl);
+  const int oa = comp_a<kMode>(a, p0);
+  const int ob = kMode == kInterleaved ? oa + 4 : comp_b<kMode>(a, p0);
 
-  float gam[8], dg[8];
+  float2 ga[2], gb[2], dga[2], dgb[2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    gam[e] = a.gamma[t] ? __ldg(a.gamma[t] + c0 + e) : 1.f;
-    dg[e] = 0.f;
+  for (int i = 0; i < 2; ++i) {
+    ga[i] = gb[i] = both(1.f);
+    dga[i] = dgb[i] = both(0.f);
+    if (a.gamma[t]) {
+      const float* g = a.gamma[t];
+      ga[i] = make_float2(__ldg(g + comp_a<kMode>(a, p0 + 2 * i)),
+                          __ldg(g + comp_a<kMode>(a, p0 + 2 * i + 1)));
+      gb[i] = make_float2(__ldg(g + comp_b<kMode>(a, p0 + 2 * i)),
+                          __ldg(g + comp_b<kMode>(a, p0 + 2 * i + 1)));
+    }
   }
 
   for (long long tb = (long long)blockIdx.x * kTokensPerBlock; tb < tokens;
@@ -174,80 +240,84 @@ __global__ void __launch_bounds__(kQkThreads) qk_rope_kernel(const __grid_consta
     const long long tok = live ? token : tokens - 1;
     const int b = (int)(tok / a.L), l = (int)(tok % a.L);
     const int pos = a.pos ? __ldg(a.pos + tok) : l;
-    // Forward: y = r (x ca + partner sa), gamma folded in.  Backward:
-    // g = dy ca - partner sa without gamma.
-    float ca[8], sa[8];
+    float2 c[2], s[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int j = c0 + e;
-      float c = 1.f, s = 0.f;
-      if (j < a.rot) {
-        const bool second = kMode == kInterleaved ? (j & 1) : j >= a.half;
-        const int i = kMode == kInterleaved ? j >> 1 : (second ? j - a.half : j);
-        const uint64_t turns = a.turn[i] * (uint64_t)(int64_t)pos;
-        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
-        if (!second) s = -s;
+    for (int e = 0; e < 4; ++e) {
+      float co = 1.f, si = 0.f;
+      if (p0 + e < a.half) {
+        const uint64_t turns = a.turn[p0 + e] * (uint64_t)(int64_t)pos;
+        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &si, &co);
       }
-      if (kBwd) {
-        ca[e] = c;
-        sa[e] = s;
-      } else {
-        const int jp = partner_of<kMode>(a, j);
-        ca[e] = gam[e] * c;
-        sa[e] = (a.gamma[t] ? __ldg(a.gamma[t] + jp) : 1.f) * s;
+      (e & 1 ? c[e >> 1].y : c[e >> 1].x) = co;
+      (e & 1 ? s[e >> 1].y : s[e >> 1].x) = si;
+    }
+    // Forward: y_a = r (x_a (ga c) - x_b (gb s)), y_b = r (x_b (gb c) + x_a (ga s)).
+    float2 ca[2], sa[2], cb[2], sb[2];
+    if (!kBwd) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ca[i] = mul2(ga[i], c[i]);
+        sa[i] = mul2(ga[i], s[i]);
+        cb[i] = mul2(gb[i], c[i]);
+        sb[i] = neg2(mul2(gb[i], s[i]));
       }
     }
     const size_t step = (size_t)a.L * kHeadDim;
     size_t off = (((size_t)b * a.H + h0) * a.L + l) * kHeadDim;
     const T* in = static_cast<const T*>(a.in[t]);
+    const T* dy = static_cast<const T*>(a.dy[t]);
     T* out = static_cast<T*>(a.out[t]);
-    if (!kBwd) {
-#pragma unroll 4
-      for (int h = h0; h < h1; ++h, off += step) {
-        Row8<T> x;
-        x.load(in + off + c0);
-        float v[8], p[8], ss = 0.f;
-        x.get(v);
+    // A few heads' rows are loaded before the first is used: inputs and
+    // outputs may alias, so the compiler cannot move the loads up.
+    for (int h = h0; h < h1; h += kAhead, off += kAhead * step) {
+      Raw<T, kMode> rx[kAhead], rd[kBwd ? kAhead : 1];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-        const float r = rsqrtf(fmaf(sum8(ss), 1.f / kHeadDim, a.eps));
-        partners<T, kMode>(a, x, v, in + off, c0, src, p);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = r * fmaf(v[e], ca[e], p[e] * sa[e]);
-        // out may be the input: with kReload other lanes read these
-        // components, so the row is read whole before any of it is written.
-        if (kMode == kReload) __syncwarp();
-        if (live) Row8<T>::store(out + off + c0, v);
-      }
-    } else {
-      const T* dy = static_cast<const T*>(a.dy[t]);
-#pragma unroll 2
-      for (int h = h0; h < h1; ++h, off += step) {
-        Row8<T> x, d;
-        x.load(in + off + c0);
-        d.load(dy + off + c0);
-        float v[8], g[8], p[8], ss = 0.f, vx = 0.f;
-        x.get(v);
-        d.get(g);
-        partners<T, kMode>(a, d, g, dy + off, c0, src, p);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          g[e] = fmaf(g[e], ca[e], -p[e] * sa[e]);
-          ss = fmaf(v[e], v[e], ss);
-          vx = fmaf(g[e] * gam[e], v[e], vx);
+      for (int u = 0; u < kAhead; ++u)
+        if (h + u < h1) {
+          rx[u].load(a, in + off + u * step, p0, oa, ob);
+          if (kBwd) rd[kBwd ? u : 0].load(a, dy + off + u * step, p0, oa, ob);
         }
-        const float r = rsqrtf(fmaf(sum8(ss), 1.f / kHeadDim, a.eps));
-        const float m = sum8(vx) * r * r * (1.f / kHeadDim);  // mean(v n) r
-        if (kMode == kReload) __syncwarp();
-        if (live) {
-          float o[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            dg[e] = fmaf(g[e] * r, v[e], dg[e]);
-            o[e] = r * fmaf(-m, v[e], g[e] * gam[e]);
+      for (int u = 0; u < kAhead; ++u) {
+        if (h + u >= h1) break;
+        const Pairs x = rx[u].get();
+        Pairs y;
+        float2 sq = mul2(x.a[0], x.a[0]);
+        sq = fma2(x.a[1], x.a[1], sq);
+        sq = fma2(x.b[0], x.b[0], sq);
+        sq = fma2(x.b[1], x.b[1], sq);
+        const float r = rsqrtf(fmaf(sum8(sq.x + sq.y), 1.f / kHeadDim, a.eps));
+        if (!kBwd) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            y.a[i] = mul2(both(r), fma2(x.b[i], sb[i], mul2(x.a[i], ca[i])));
+            y.b[i] = mul2(both(r), fma2(x.a[i], sa[i], mul2(x.b[i], cb[i])));
           }
-          Row8<T>::store(out + off + c0, o);
+        } else {
+          const Pairs d = rd[kBwd ? u : 0].get();
+          float2 va[2], vb[2], vx = both(0.f);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // g = R^T dy; v = gamma g
+            const float2 g = fma2(d.b[i], s[i], mul2(d.a[i], c[i]));
+            const float2 k = fma2(d.a[i], neg2(s[i]), mul2(d.b[i], c[i]));
+            va[i] = mul2(g, ga[i]);
+            vb[i] = mul2(k, gb[i]);
+            vx = fma2(va[i], x.a[i], vx);
+            vx = fma2(vb[i], x.b[i], vx);
+            if (live) {
+              dga[i] = fma2(g, mul2(both(r), x.a[i]), dga[i]);
+              dgb[i] = fma2(k, mul2(both(r), x.b[i]), dgb[i]);
+            }
+          }
+          const float m = -sum8(vx.x + vx.y) * r * r * (1.f / kHeadDim);  // -mean(v n) r
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            y.a[i] = mul2(both(r), fma2(both(m), x.a[i], va[i]));
+            y.b[i] = mul2(both(r), fma2(both(m), x.b[i], vb[i]));
+          }
         }
+        if (live) Raw<T, kMode>::store(a, out + off + u * step, p0, oa, ob, y);
       }
     }
   }
@@ -256,20 +326,24 @@ __global__ void __launch_bounds__(kQkThreads) qk_rope_kernel(const __grid_consta
     // The block's sum of g n per component, in a fixed order: over the
     // warp's four tokens, then over its warps.
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      dg[e] += __shfl_xor_sync(0xffffffffu, dg[e], 8);
-      dg[e] += __shfl_xor_sync(0xffffffffu, dg[e], 16);
-    }
-    if (lane < 8) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) red[threadIdx.x >> 5][c0 + e] = dg[e];
+    for (int e = 0; e < 4; ++e) {
+      float x = e & 1 ? dga[e >> 1].y : dga[e >> 1].x;
+      float y = e & 1 ? dgb[e >> 1].y : dgb[e >> 1].x;
+      x += __shfl_xor_sync(0xffffffffu, x, 8);
+      x += __shfl_xor_sync(0xffffffffu, x, 16);
+      y += __shfl_xor_sync(0xffffffffu, y, 8);
+      y += __shfl_xor_sync(0xffffffffu, y, 16);
+      if (lane < 8) {
+        red[threadIdx.x >> 5][comp_a<kMode>(a, p0 + e)] = x;
+        red[threadIdx.x >> 5][comp_b<kMode>(a, p0 + e)] = y;
+      }
     }
     __syncthreads();
     if (threadIdx.x < 64) {
-      float s = 0.f;
+      float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kQkThreads / 32; ++w) s += red[w][threadIdx.x];
-      a.part[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 64 + threadIdx.x] = s;
+      for (int w = 0; w < kQkThreads / 32; ++w) sum += red[w][threadIdx.x];
+      a.part[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 64 + threadIdx.x] = sum;
     }
   }
 }
@@ -302,11 +376,11 @@ int token_blocks(const bb_qk_desc& d, bool bwd) {
   return (int)(tiles < cap ? tiles : cap);
 }
 
-// Head ranges per tensor: enough blocks to fill the GPU (eight 256-thread
+// Head ranges per tensor: enough blocks to fill the GPU (four 256-thread
 // blocks on each of 148 SMs), at most one per head; longer walks share the
 // angles.
 int head_splits(const bb_qk_desc& d, bool bwd) {
-  const int want = 148 * 8, have = 2 * token_blocks(d, bwd);
+  const int want = 148 * 4, have = 2 * token_blocks(d, bwd);
   int s = (want + have - 1) / have;
   return s < d.H ? s : d.H;
 }
@@ -335,9 +409,9 @@ QkArgs make_args(const bb_qk_desc& d, bool bwd) {
   // Turns per position as a fraction of 2^64, in extended precision: at
   // most 1 / 2 pi, so it fits.
   const long double tau = 6.283185307179586476925286766559005768L;
-  for (int i = 0; i < a.half; ++i)
-    a.turn[i] = (uint64_t)(powl((long double)d.theta, -2.0L * i / d.rot_dim) / tau *
-                           18446744073709551616.0L);
+  const long double q = a.half ? powl((long double)d.theta, -2.0L / d.rot_dim) : 0.0L;
+  long double f = 18446744073709551616.0L / tau;
+  for (int i = 0; i < a.half; ++i, f *= q) a.turn[i] = (uint64_t)f;
   return a;
 }
 
@@ -346,10 +420,10 @@ cudaError_t launch_mode(const bb_qk_desc& d, const QkArgs& a, cudaStream_t s) {
   const dim3 grid(token_blocks(d, kBwd), 2 * a.hsplit);
   if (d.interleaved || a.rot == 0)
     qk_rope_kernel<T, kInterleaved, kBwd><<<grid, kQkThreads, 0, s>>>(a);
-  else if (a.half % 8 == 0)
-    qk_rope_kernel<T, kShuffle, kBwd><<<grid, kQkThreads, 0, s>>>(a);
+  else if (a.half % 4 == 0)
+    qk_rope_kernel<T, kHalves, kBwd><<<grid, kQkThreads, 0, s>>>(a);
   else
-    qk_rope_kernel<T, kReload, kBwd><<<grid, kQkThreads, 0, s>>>(a);
+    qk_rope_kernel<T, kScattered, kBwd><<<grid, kQkThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
