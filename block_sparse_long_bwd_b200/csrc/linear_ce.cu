@@ -35,24 +35,39 @@ namespace {
 
 using namespace sm100;
 
-// A tile of the GEMMs is 256 x 256: a pair of CTAs (cta_group::2), 128 rows of
-// A and 128 columns of B in each one's shared memory, 128 x 256 accumulators
-// in each one's tensor memory, two of them, so that a tile's epilogue runs
-// under the next tile's MMAs.
-constexpr int kBM = 128;                            // rows of a CTA
-constexpr int kTM = 2 * kBM, kTN = 256, kBK = 64;   // tile of a pair, K step
-constexpr int kStages = 5;
-constexpr uint32_t kBox = 64 * 64 * 2;              // one 64 x 64 bf16 box: 8 KB
-constexpr uint32_t kOpTile = 128 * kBK * 2;         // a CTA's part of A or B: 16 KB
-constexpr uint32_t kStageBytes = 2 * kOpTile;       // 32 KB
-constexpr int kEpiWarps = 8;                        // two per TMEM lane quarter
-constexpr uint32_t kStageOut = kEpiWarps * 4096;    // a 32 x 128 B block per warp
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr uint32_t kTmemCols = 512;                 // two 128 x 256 fp32 accumulators
-constexpr int kHalf = kTN / 2;                      // columns of an epilogue warp
-constexpr size_t kPieceBytes = 256u << 20;          // dz of one vocabulary piece
+constexpr int kBM = 128, kBK = 64;             // rows of a CTA's tile, K step
+constexpr uint32_t kBox = 64 * 64 * 2;         // one 64 x 64 bf16 box: 8 KB
+constexpr uint32_t kATile = kBM * kBK * 2;     // 16 KB
+constexpr size_t kPieceBytes = 256u << 20;     // dz of one vocabulary piece
 
 enum Mode { kLse = 0, kDz = 1, kGrad = 2 };
+
+// Tile shapes.  Pairs of CTAs (cta_group::2) form 256 x 256 tiles: 128 rows of
+// A and 128 columns of B in each CTA's shared memory.  Up to 128 rows a pair's
+// second half would be empty, and the vocabulary's weights bound the launch:
+// single CTAs take 128 x 64 logits (enough tiles to keep every SM loading)
+// and 128 x 256 gradients.  Two accumulators, so that a tile's epilogue runs
+// under the next one's MMAs.
+template <int kMode, bool kPair>
+struct Cfg {
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int kTM = kBM * kCtas;
+  static constexpr int kTN = kPair || kMode == kGrad ? 256 : 64;
+  static constexpr int kEpi = kTN == 256 ? 8 : 4;          // epilogue warps
+  static constexpr int kCols = kTN / (kEpi / 4);           // columns of one (logits)
+  static constexpr int kSlots = kMode == kGrad ? 2 : 0;
+  static constexpr uint32_t kBTile = kTN / kCtas * kBK * 2;
+  static constexpr uint32_t kStage = kATile + kBTile;
+  static constexpr int kStages = kPair ? 5 : kMode == kGrad ? 3 : 8;
+  static constexpr uint32_t kOut = kEpi * kSlots * 4096;   // 32 x 128 B staging blocks
+  static constexpr uint32_t kSmem = 1024 + kStages * kStage + kOut;
+  static constexpr int kThreads = 64 + 32 * kEpi;
+  static constexpr uint32_t kTmem = 2 * kTN;               // columns: two accumulators
+};
+
+// Cost of a gradient tile in K steps: a short one waits for its loads and
+// stores instead.
+__host__ __device__ constexpr int tile_cost(int ksteps) { return ksteps < 3 ? 3 : ksteps; }
 
 // What rows_kernel finds out on the device, at the workspace's start.
 struct Info {
@@ -69,20 +84,22 @@ struct CeArgs {
   int Vp;            // columns of a piece (a multiple of 256)
   int v0, vn;        // this piece: first column, columns
   int splits;        // parts the piece's columns are cut into for dh
+  int a_bytes;       // logits: bytes of h's box per K step (its rows, at most kBM)
   int add;           // dh partials: 1 adds to what earlier pieces wrote
   Info* info;
   const float* bias;   // [V] or null
   const int* lab;      // packed rows: label,
   const float* rlse;   //   lse,
-  const float* dls;    //   dloss / dlref
-  float2* part;        // [vocabulary half tiles][Np] (max, sum of exponentials)
-  float* zl;           // [N] logit of the label
+  const float* dls;    //   dloss / dlref,
+  const float* zl;     //   logit of the label (rows_kernel)
+  uint16_t* dz;        // [Vp / 64][Np][64]: panels of 64 columns
+  float2* part;        // [column runs of an epilogue warp][Np] (max, sum of exponentials)
   float* dbp;          // [Np / 128][Vp] column sums of dz, or null
   float* dbias;        // [V], with dbp
 };
 
 struct Bars {
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], red;
+  uint64_t full[8], empty[8], acc_full[2], acc_empty[2], red;
 };
 
 // One output tile.
@@ -90,56 +107,87 @@ struct Job {
   int dw;           // kGrad: 1 = a tile of dW, 0 = of dh
   int m0, n0;       // first row and column of the tile
   int k0, ksteps;   // first K index, 64-wide K steps
-  int nblk;         // 64-column blocks of B in each CTA: the tile has 128 nblk columns
+  int nblk;         // 64-column blocks of B in each CTA
   int row0;         // first row in the output
 };
 
-template <int kMode>
+// A launch's tiles and the share of each worker (a pair or a single CTA).
+//
+// Logits: every worker takes every `stride`-th tile.  Gradients: tiles of two
+// costs, dh's (K: the piece's columns, cut into `splits`) and dW's (K: the
+// rows).  The dearer kind is dealt out first; workers that got one fewer of
+// it take `lead` more of the cheaper kind before that is dealt out to all, so
+// the workers end within about one cheap tile of each other.
+template <int kMode, bool kPair>
 struct Work {
-  int tiles, mt, dn, wm, th, hks, wks, dh_first;
-  __device__ __forceinline__ Work(const CeArgs& a, int rows) {
-    mt = (rows + kTM - 1) / kTM;
+  using C = Cfg<kMode, kPair>;
+  int w, stride;                  // this worker, workers
+  int tiles, mt, dn, hks, wks;
+  int dw_first, na, nb, more, lead;  // kinds in order; workers with one more of the first
+  __device__ __forceinline__ Work(const CeArgs& a, int rows, int worker, int workers)
+      : w(worker), stride(workers) {
+    mt = (rows + C::kTM - 1) / C::kTM;
     if (kMode != kGrad) {
-      tiles = mt * ((a.vn + kTN - 1) / kTN);
+      tiles = mt * ((a.vn + C::kTN - 1) / C::kTN);
       return;
     }
-    dn = (a.D + kTN - 1) / kTN;
-    wm = (a.vn + kTM - 1) / kTM;
+    dn = (a.D + C::kTN - 1) / C::kTN;
     hks = (a.vn + kBK - 1) / kBK;
     wks = (rows + kBK - 1) / kBK;
-    th = mt * dn * a.splits;
-    tiles = th + wm * dn;
-    // Long tiles first.
-    dh_first = hks / a.splits >= wks;
+    const int nh = mt * dn * a.splits, nw = (a.vn + C::kTM - 1) / C::kTM * dn;
+    const int ch = tile_cost(hks / a.splits), cw = tile_cost(wks);
+    dw_first = cw > ch;
+    na = dw_first ? nw : nh;
+    nb = dw_first ? nh : nw;
+    more = na % stride;
+    const int ca = dw_first ? cw : ch, cb = dw_first ? ch : cw, fewer = stride - more;
+    lead = more ? (ca + cb / 2) / cb : 0;
+    if (lead > nb / fewer) lead = nb / fewer;
+  }
+  // The i-th tile of this worker, or -1 after its last.
+  __device__ __forceinline__ int tile(int i) const {
+    if (kMode != kGrad) {
+      const int t = w + i * stride;
+      return t < tiles ? t : -1;
+    }
+    const int mine = na / stride + (w < more);
+    if (i < mine) return i * stride + w;
+    i -= mine;
+    int u;
+    if (w >= more) {
+      if (i < lead) return na + i * (stride - more) + (w - more);
+      i -= lead;
+    }
+    u = lead * (stride - more) + i * stride + w;
+    return u < nb ? na + u : -1;
   }
   __device__ __forceinline__ Job job(const CeArgs& a, int t) const {
     Job j;
-    j.nblk = 2;
+    j.nblk = C::kTN / C::kCtas / 64;
     if (kMode != kGrad) {
       // Row tiles run fastest: the rows stay in L2 while W streams by once.
       j.dw = 0;
-      j.m0 = (t % mt) * kTM;
-      j.n0 = (t / mt) * kTN;
+      j.m0 = (t % mt) * C::kTM;
+      j.n0 = (t / mt) * C::kTN;
       j.k0 = 0;
       j.ksteps = (a.D + kBK - 1) / kBK;
       j.row0 = j.m0;
       return j;
     }
-    j.dw = dh_first ? t >= th : t < wm * dn;
-    int u = t;
-    if (dh_first && j.dw) u -= th;
-    if (!dh_first && !j.dw) u -= wm * dn;
-    j.n0 = (u % dn) * kTN;
-    if (a.D - j.n0 <= 128) j.nblk = 1;
+    j.dw = dw_first ? t < na : t >= na;
+    int u = t < na ? t : t - na;
+    j.n0 = (u % dn) * C::kTN;
+    const int left = (a.D - j.n0 + 64 * C::kCtas - 1) / (64 * C::kCtas);
+    j.nblk = left < j.nblk ? left : j.nblk;
     u /= dn;
     if (j.dw) {
-      j.m0 = u * kTM;
+      j.m0 = u * C::kTM;
       j.k0 = 0;
       j.ksteps = wks;
       j.row0 = a.v0 + j.m0;
     } else {
       const int s = u / mt;
-      j.m0 = (u % mt) * kTM;
+      j.m0 = (u % mt) * C::kTM;
       j.k0 = (int)((long long)hks * s / a.splits);
       j.ksteps = (int)((long long)hks * (s + 1) / a.splits) - j.k0;
       j.row0 = s * a.Np + j.m0;
@@ -150,7 +198,13 @@ struct Work {
 
 // Sum over the 32 lanes of each of 32 columns held one row per lane; lane l
 // returns column l.  Each step halves the columns a lane carries.
-__device__ __forceinline__ float column_sums(float (&x)[32], int lane) {
+__device__ __forceinline__ float column_sums(const float2 (&z)[16], int lane) {
+  float x[32];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    x[2 * e] = z[e].x;
+    x[2 * e + 1] = z[e].y;
+  }
 #pragma unroll
   for (int s = 16; s >= 1; s >>= 1) {
     const bool up = lane & s;
@@ -164,125 +218,142 @@ __device__ __forceinline__ float column_sums(float (&x)[32], int lane) {
   return x[0];
 }
 
-// 32 logits of one row: the accumulator's columns plus bias.  Columns past V
-// get `fill`.
-__device__ __forceinline__ void logits32(const CeArgs& a, uint32_t taddr, int c0, float fill,
-                                         float (&z)[32]) {
-  uint32_t v[32];
-  __syncwarp();
-  tmem_ld32(taddr, v);
-  tmem_ld_wait();
+// 32 logits of a row from its accumulator columns and their bias (in shared
+// memory, the same for every lane).
+__device__ __forceinline__ void add_bias(const uint32_t (&v)[32], const float* bias,
+                                         float2 (&z)[16]) {
 #pragma unroll
-  for (int e = 0; e < 32; ++e) z[e] = __uint_as_float(v[e]);
-  if (c0 + 32 <= a.V) {
-    if (a.bias) {
-#pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + c0 + e));
-        z[e] += b.x; z[e + 1] += b.y; z[e + 2] += b.z; z[e + 3] += b.w;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-      z[e] = c0 + e < a.V ? z[e] + (a.bias ? __ldg(a.bias + c0 + e) : 0.f) : fill;
+  for (int e = 0; e < 32; e += 4) {
+    const float4 b = *reinterpret_cast<const float4*>(bias + e);
+    z[e / 2] = add2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                    make_float2(b.x, b.y));
+    z[e / 2 + 1] = add2(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
+                        make_float2(b.z, b.w));
   }
 }
 
-template <int kMode>
-__global__ void __launch_bounds__(kThreads, 1)
+// Element i of a row's 32 values, where 0 <= i < 32, becomes x.
+__device__ __forceinline__ void put(float2 (&z)[16], int i, float x) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    z[e].x = i == 2 * e ? x : z[e].x;
+    z[e].y = i == 2 * e + 1 ? x : z[e].y;
+  }
+}
+
+template <int kMode, bool kPair>
+__global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CeArgs a, const __grid_constant__ CUtensorMap tmH,
                    const __grid_constant__ CUtensorMap tmHp,
                    const __grid_constant__ CUtensorMap tmW,
                    const __grid_constant__ CUtensorMap tmDz,
                    const __grid_constant__ CUtensorMap tmDw,
                    const __grid_constant__ CUtensorMap tmDh) {
+  using C = Cfg<kMode, kPair>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
-  __shared__ float red[2][4][kTN];  // kDz: column sums of each warp's 32 rows
+  __shared__ float red[2][4][kMode == kDz ? C::kTN : 1];  // column sums of 32 rows
+  __shared__ __align__(16) float bias_sh[kMode == kGrad ? 1 : C::kEpi][C::kCols];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t rank = kPair ? cluster_rank() : 0;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint8_t* stages = base;                              // [kStages][A | B]
-  uint8_t* stage_out = base + kStages * kStageBytes;   // [8 warps][32][128 B]
+  uint8_t* stages = base;                                 // [kStages][A | B]
+  uint8_t* stage_out = base + C::kStages * C::kStage;     // [warps][slots][32][128 B]
   int* status = &a.info->status;
-  const int rows = a.info->rows;
-  const CUtensorMap* mapH = a.info->direct ? &tmH : &tmHp;
-  const Work<kMode> work(a, rows);
 
-  // Barriers of the pair: `full` and `acc_empty` are used in rank 0 only (it
+  // Barriers of a pair: `full` and `acc_empty` are used in rank 0 only (it
   // issues the MMAs); both CTAs' loads and epilogue warps signal them there.
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&bars.full[s], 1);
       mbar_init(&bars.empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.acc_full[s], 1);
-      mbar_init(&bars.acc_empty[s], 2 * kEpiWarps);
+      mbar_init(&bars.acc_empty[s], C::kCtas * C::kEpi);
     }
-    mbar_init(&bars.red, kEpiWarps);
+    mbar_init(&bars.red, C::kEpi);
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc_pair(&tmem_base_sh, kTmemCols);
-    tmem_relinquish_pair();
+    if (kPair) {
+      tmem_alloc_pair(&tmem_base_sh, C::kTmem);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&tmem_base_sh, C::kTmem);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  if (kPair) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
+  grid_launch_dependents();
+  grid_wait();
+  const int rows = a.info->rows;
+  const CUtensorMap* mapH = a.info->direct ? &tmH : &tmHp;
+  const Work<kMode, kPair> work(a, rows, blockIdx.x / C::kCtas, gridDim.x / C::kCtas);
 
   if (warp == 0) {
     // ---------------- TMA loads (one thread of each CTA) ----------------
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int t = pair; t < work.tiles && ok; t += pairs) {
+      for (int i = 0, t; ok && (t = work.tile(i)) >= 0; ++i) {
         const Job j = work.job(a, t);
+        // Single CTAs all read the same few rows of h: each tile begins at
+        // another K step, or all would wait for the same lines of L2.
+        const int k_first = !kPair && kMode != kGrad ? t % j.ksteps : 0;
         const int m0 = j.m0 + rank * kBM, n0 = j.n0 + rank * 64 * j.nblk;
+        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+          if (kPair)
+            tma_load_2d_pair(dst, map, map_rank(bar, 0), x, y);
+          else
+            tma_load_2d(dst, map, bar, x, y);
+        };
         for (int ks = 0; ks < j.ksteps; ++ks, ++it) {
-          const uint32_t st = it % kStages;
-          if (!mbar_wait(&bars.empty[st], ((it / kStages) & 1) ^ 1, &abort_flag, status)) {
+          const uint32_t st = it % C::kStages;
+          if (!mbar_wait(&bars.empty[st], ((it / C::kStages) & 1) ^ 1, &abort_flag, status)) {
             ok = false;
             break;
           }
-          uint8_t* pa = stages + st * kStageBytes;
-          uint8_t* pb = pa + kOpTile;
-          const uint32_t bar = map_rank(&bars.full[st], 0);
-          if (rank == 0) mbar_expect_tx(&bars.full[st], 2 * (kOpTile + j.nblk * kBox));
-          const int k = (j.k0 + ks) * kBK;
+          uint8_t* pa = stages + st * C::kStage;
+          uint8_t* pb = pa + kATile;
+          uint64_t* bar = &bars.full[st];
+          if (rank == 0)
+            mbar_expect_tx(bar, C::kCtas * ((kMode == kGrad ? kATile : a.a_bytes) + j.nblk * kBox));
+          const int kr = k_first + ks;
+          const int k = (j.k0 + (kr < j.ksteps ? kr : kr - j.ksteps)) * kBK;
           if (kMode != kGrad) {
-            tma_load_2d_pair(pa, mapH, bar, k, m0);
-            tma_load_2d_pair(pb, &tmW, bar, k, a.v0 + n0);
+            load(pa, mapH, bar, k, m0);
+            load(pb, &tmW, bar, k, a.v0 + n0);
           } else {
             // dW: A = dz^T (columns of dz along M), B = h; dh: A = dz, B = W.
+            // A 64 x 64 box of a panel of dz is 8 KB in one piece.
             for (int i = 0; i < 2; ++i)
-              tma_load_2d_pair(pa + i * kBox, &tmDz, bar, j.dw ? m0 + 64 * i : k,
-                               j.dw ? k : m0 + 64 * i);
+              load(pa + i * kBox, &tmDz, bar, 0,
+                   j.dw ? (m0 / 64 + i) * a.Np + k : k / 64 * a.Np + m0 + 64 * i);
             for (int i = 0; i < j.nblk; ++i)
-              tma_load_2d_pair(pb + i * kBox, j.dw ? mapH : &tmW, bar, n0 + 64 * i,
-                               j.dw ? k : a.v0 + k);
+              load(pb + i * kBox, j.dw ? mapH : &tmW, bar, n0 + 64 * i, j.dw ? k : a.v0 + k);
           }
         }
       }
       // The last stages' releases reach this CTA before it may leave.
-      for (int i = 0; i < kStages && ok; ++i, ++it)
-        ok = mbar_wait(&bars.empty[it % kStages], ((it / kStages) & 1) ^ 1, &abort_flag, status);
+      for (int i = 0; i < C::kStages && ok; ++i, ++it)
+        ok = mbar_wait(&bars.empty[it % C::kStages], ((it / C::kStages) & 1) ^ 1, &abort_flag, status);
       if (abort_flag && rank == 0) {
         // Let issued copies (both CTAs') land before shared memory goes away;
         // rank 1 waits at the cluster barrier meanwhile.
-        for (uint32_t s = 0; s < (uint32_t)kStages; ++s)
+        for (uint32_t s = 0; s < (uint32_t)C::kStages; ++s)
           if (it >= s + 1) {
-            const uint32_t last = it - 1 - ((it - 1 - s) % kStages);
+            const uint32_t last = it - 1 - ((it - 1 - s) % C::kStages);
             const uint64_t t0 = globaltimer();
-            while (!mbar_try_wait(&bars.full[s], (last / kStages) & 1) &&
+            while (!mbar_try_wait(&bars.full[s], (last / C::kStages) & 1) &&
                    globaltimer() - t0 < 100000000ull) {
             }
           }
@@ -292,151 +363,183 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- MMA issue (one thread of rank 0) ----------------
     uint32_t it = 0, tc = 0;
     bool ok = rank == 0;
-    for (int t = pair; t < work.tiles && ok; t += pairs, ++tc) {
+    for (int t; ok && (t = work.tile(tc)) >= 0; ++tc) {
       const Job j = work.job(a, t);
       const int acc = tc & 1;
       if (!mbar_wait(&bars.acc_empty[acc], ((tc >> 1) & 1) ^ 1, &abort_flag, status)) break;
       tc_fence_after();
       // K-major tiles step 32 bytes per 16 of K; MN-major ones 16 rows of 128.
       const uint32_t a_mn = kMode == kGrad && j.dw, b_mn = kMode == kGrad;
-      const uint32_t idesc = idesc_bf16(kTM, 128 * j.nblk, a_mn, b_mn);
+      const uint32_t idesc = idesc_bf16(C::kTM, 64 * C::kCtas * j.nblk, a_mn, b_mn);
       const uint32_t astep = a_mn ? 2048 : 32, bstep = b_mn ? 2048 : 32;
       const uint32_t albo = a_mn ? kBox : 16, blbo = b_mn ? kBox : 16;
       for (int ks = 0; ks < j.ksteps; ++ks, ++it) {
-        const uint32_t st = it % kStages;
-        if (!mbar_wait(&bars.full[st], (it / kStages) & 1, &abort_flag, status)) {
+        const uint32_t st = it % C::kStages;
+        if (!mbar_wait(&bars.full[st], (it / C::kStages) & 1, &abort_flag, status)) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (lane == 0) {
-          const uint32_t aaddr = smem_u32(stages + st * kStageBytes);
-          const uint32_t baddr = aaddr + kOpTile;
+          const uint32_t aaddr = smem_u32(stages + st * C::kStage);
+          const uint32_t baddr = aaddr + kATile;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ss_pair(tmem + acc * kTN, sdesc_sw128(aaddr + kk * astep, albo),
-                        sdesc_sw128(baddr + kk * bstep, blbo), idesc,
-                        (ks > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_pair(&bars.empty[st]);
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t da = sdesc_sw128(aaddr + kk * astep, albo);
+            const uint64_t db = sdesc_sw128(baddr + kk * bstep, blbo);
+            const uint32_t more = (ks > 0 || kk > 0) ? 1u : 0u;
+            if (kPair)
+              mma_ss_pair(tmem + acc * C::kTN, da, db, idesc, more);
+            else
+              mma_ss(tmem + acc * C::kTN, da, db, idesc, more);
+          }
+          if (kPair)
+            mma_commit_pair(&bars.empty[st]);
+          else
+            mma_commit(&bars.empty[st]);
         }
         __syncwarp();
       }
-      if (ok && lane == 0) mma_commit_pair(&bars.acc_full[acc]);
+      if (ok && lane == 0) {
+        if (kPair)
+          mma_commit_pair(&bars.acc_full[acc]);
+        else
+          mma_commit(&bars.acc_full[acc]);
+      }
       __syncwarp();
     }
   } else {
-    // ------- epilogue (warps 2-9: 32 rows and half of the columns each) -------
+    // ------- epilogue (32 rows and, of eight warps, half of the columns each) -------
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    uint8_t* stage = stage_out + (warp - 2) * 4096;
+    uint8_t* stage = stage_out + (warp - 2) * C::kSlots * 4096;
     uint8_t* rowp = stage + lane * 128;
     const int swz = lane & 7;
     const float dlref = kMode == kGrad ? a.info->dlref : 1.f;
-    const uint32_t acc_empty = map_rank(&bars.acc_empty[0], 0);
+    auto release = [&](int acc) {  // the accumulator is read
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (kPair)
+          mbar_arrive_cluster(map_rank(&bars.acc_empty[acc], 0));
+        else
+          mbar_arrive(&bars.acc_empty[acc]);
+      }
+    };
+    int slot = 0;  // kGrad: staging slot of the latest store
+    float m = -INFINITY, s = 0.f;  // kLse: maximum and sum of exponentials
     uint32_t tc = 0;
-    for (int t = pair; t < work.tiles; t += pairs, ++tc) {
+    for (int t; (t = work.tile(tc)) >= 0; ++tc) {
       const Job j = work.job(a, t);
       const int acc = tc & 1;
+      const int r0 = rank * kBM + quarter * 32;  // this warp's first row in the tile
+      const int row = j.m0 + r0 + lane;          // packed row (logits)
+      const bool live = row < rows;
+      const int cbeg = half * C::kCols;
+      int lab = -1;
+      float zl = 0.f, lse = 0.f, dl = 0.f;
+      if (kMode != kGrad) {
+        // What the tile's epilogue reads besides the logits, under its MMAs.
+        // Words past V are excluded.
+        float b[C::kCols / 32];
+#pragma unroll
+        for (int i = 0; i < C::kCols / 32; ++i) {
+          const int v = a.v0 + j.n0 + cbeg + 32 * i + lane;
+          b[i] = v < a.V ? (a.bias ? __ldg(a.bias + v) : 0.f) : -INFINITY;
+        }
+        if (live) {
+          lab = __ldg(a.lab + row);
+          zl = __ldg(a.zl + row);
+          if (kMode == kDz) {
+            lse = __ldg(a.rlse + row);
+            dl = __ldg(a.dls + row);
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < C::kCols / 32; ++i) bias_sh[warp - 2][32 * i + lane] = b[i];
+        __syncwarp();
+      }
       if (!mbar_wait(&bars.acc_full[acc], (tc >> 1) & 1, &abort_flag, status)) break;
       tc_fence_after();
-      const uint32_t tz = tmem + acc * kTN + lane_off;
-      const int r0 = rank * kBM + quarter * 32;  // this warp's first row in the tile
-      const int row = j.m0 + r0 + lane;          // packed row (kLse, kDz)
-      const int cbeg = half * kHalf;
-      if (kMode == kLse) {
-        const int lab = row < rows ? __ldg(a.lab + row) : -1;
-        float m = -INFINITY, s = 0.f;
-#pragma unroll 1
-        for (int c = cbeg; c < cbeg + kHalf; c += 32) {
-          const int c0 = j.n0 + c;
-          if (c0 >= a.V) break;
-          float z[32];
-          logits32(a, tz + c, c0, -INFINITY, z);
-          if ((unsigned)(lab - c0) < 32u) {
-            float zl = z[0];
-#pragma unroll
-            for (int e = 1; e < 32; ++e) zl = lab - c0 == e ? z[e] : zl;
-            a.zl[row] = zl;
-          }
-          float cm = m;
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) cm = fmax3(cm, z[e], z[e + 1]);
-          // A row of -inf so far keeps a finite reference.  Differences are
-          // taken before the scaling to base 2, so logits near the type's
-          // lowest value do not overflow.
-          const float ref = cm == -INFINITY ? 0.f : cm;
-          float2 sum = make_float2(s * ex2((m - ref) * kLog2e), 0.f);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 d = mul2(sub2(make_float2(z[e], z[e + 1]), make_float2(ref, ref)),
-                                  make_float2(kLog2e, kLog2e));
-            sum = add2(sum, make_float2(ex2(d.x), ex2(d.y)));
-          }
-          s = sum.x + sum.y;
-          m = cm;
+      const uint32_t tz = tmem + acc * C::kTN + lane_off;
+      if (kMode != kGrad) {
+        // Single CTAs see the same rows in every tile: one pair runs through.
+        if (kPair) {
+          m = -INFINITY;
+          s = 0.f;
         }
-        tc_fence_before();
+        uint32_t v[32];
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_empty + 8 * acc);
-        a.part[(size_t)((j.n0 + cbeg) / kHalf) * a.Np + row] = make_float2(m, s);
-        continue;
-      }
-      if (kMode == kDz) {
-        const bool live = row < rows;
-        const int lab = live ? __ldg(a.lab + row) - a.v0 : -1;
-        const float lse = live ? __ldg(a.rlse + row) : 0.f;
-        const float dl = live ? __ldg(a.dls + row) : 0.f;
+        tmem_ld32(tz + cbeg, v);
 #pragma unroll 1
-        for (int c = cbeg; c < cbeg + kHalf; c += 32) {
-          const int c0 = j.n0 + c;  // column in the piece
-          float z[32];
-          logits32(a, tz + c, a.v0 + c0, 0.f, z);
-          const int last = a.V - a.v0 - c0;  // columns of this block inside V
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 d = mul2(sub2(make_float2(z[e], z[e + 1]), make_float2(lse, lse)),
-                                  make_float2(kLog2e, kLog2e));
-            z[e] = dl * (ex2(d.x) - (lab - c0 == e ? 1.f : 0.f));
-            z[e + 1] = dl * (ex2(d.y) - (lab - c0 == e + 1 ? 1.f : 0.f));
-          }
-          // Rows past the last and columns past V: exact zeros, whatever the
-          // accumulator held.
-          if (!live || last < 32) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) z[e] = live && e < last ? z[e] : 0.f;
-          }
-          if ((c & 32) == 0) {
-            // The previous block's store has read the staging area.
-            if (lane == 0) bulk_wait_read_all();
+        for (int c = 0; c < C::kCols; c += 32) {
+          float2 z[16];
+          tmem_ld_wait();
+          add_bias(v, bias_sh[warp - 2] + c, z);
+          if (c + 32 < C::kCols) tmem_ld32(tz + cbeg + c + 32, v);
+          // The label's column of these 32.  Its logit is the one that
+          // rows_kernel summed in fp32: the tensor core truncates its running
+          // sum at every step, and the largest logits, mostly the labels',
+          // show it first.
+          const int hot = lab - a.v0 - j.n0 - cbeg - c;
+          if (kMode == kLse) {
+            if ((unsigned)hot < 32u) put(z, hot, zl);
             __syncwarp();
-          }
+            float cm = m;
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch)
-            *reinterpret_cast<uint4*>(rowp + (((((c >> 5) & 1) * 4 + ch) ^ swz) << 4)) =
-                make_uint4(pack_bf16(z[8 * ch], z[8 * ch + 1]),
-                           pack_bf16(z[8 * ch + 2], z[8 * ch + 3]),
-                           pack_bf16(z[8 * ch + 4], z[8 * ch + 5]),
-                           pack_bf16(z[8 * ch + 6], z[8 * ch + 7]));
-          if (c & 32) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&tmDz, stage, j.n0 + c - 32, j.m0 + r0);
-              bulk_commit_group();
+            for (int e = 0; e < 16; ++e) cm = fmax3(cm, z[e].x, z[e].y);
+            // A row of -inf so far keeps a finite reference.  Differences are
+            // taken before the scaling to base 2, so logits near the type's
+            // lowest value do not overflow.
+            const float ref = cm == -INFINITY ? 0.f : cm;
+            float2 sum = make_float2(s * ex2((m - ref) * kLog2e), 0.f);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 d = mul2(sub2(z[e], make_float2(ref, ref)),
+                                    make_float2(kLog2e, kLog2e));
+              sum = add2(sum, make_float2(ex2(d.x), ex2(d.y)));
             }
+            s = sum.x + sum.y;
+            m = cm;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 d = mul2(sub2(z[e], make_float2(lse, lse)),
+                                    make_float2(kLog2e, kLog2e));
+              z[e] = mul2(make_float2(ex2(d.x), ex2(d.y)), make_float2(dl, dl));
+            }
+            if ((unsigned)hot < 32u) put(z, hot, dl * (ex2((zl - lse) * kLog2e) - 1.f));
+            // Rows past the last: exact zeros, whatever the accumulator held.
+            if (!live) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) z[e] = make_float2(0.f, 0.f);
+            }
+            __syncwarp();
+            uint16_t* out = a.dz + ((size_t)((j.n0 + cbeg + c) / 64) * a.Np + row) * 64 + (c & 32);
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+              uint32_t u[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) u[e] = pack_bf16(z[8 * ch + e].x, z[8 * ch + e].y);
+              st_global_32(out + 16 * ch, u);
+            }
+            if (a.dbp) red[acc][quarter][cbeg + c + lane] = column_sums(z, lane);
           }
-          if (a.dbp) red[acc][quarter][c + lane] = column_sums(z, lane);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_empty + 8 * acc);
-        if (a.dbp) {
+        release(acc);
+        if (kMode == kLse) {
+          if (kPair)
+            a.part[(size_t)((j.n0 + cbeg) / C::kCols) * a.Np + row] = make_float2(m, s);
+          else if (work.tile(tc + 1) < 0)
+            a.part[(size_t)work.w * a.Np + row] = make_float2(m, s);
+        } else if (a.dbp) {
           // Column sums of the CTA's 128 rows: the four quarters' sums in order.
           if (lane == 0) mbar_arrive_release(&bars.red);
           if (!mbar_wait(&bars.red, tc & 1, &abort_flag, status)) break;
-          const int c = (warp - 2) * 32 + lane;
-          a.dbp[(size_t)(j.m0 / kBM + rank) * a.Vp + j.n0 + c] =
-              red[acc][0][c] + red[acc][1][c] + red[acc][2][c] + red[acc][3][c];
+          for (int c = (warp - 2) * 32 + lane; c < C::kTN; c += 32 * C::kEpi)
+            a.dbp[(size_t)(j.m0 / kBM + rank) * a.Vp + j.n0 + c] =
+                red[acc][0][c] + red[acc][1][c] + red[acc][2][c] + red[acc][3][c];
         }
         continue;
       }
@@ -451,16 +554,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // A tile without K steps (no rows) is zero.
       const float f = j.ksteps > 0 ? 1.f : 0.f;
+      // The next staging slot, once the store before last has read it.
+      auto next_slot = [&]() {
+        slot ^= 1;
+        if (lane == 0) bulk_wait_read_but_one();
+        __syncwarp();
+        return rowp + slot * 4096;
+      };
 #pragma unroll 1
-      for (int cb = half * j.nblk; cb < (half + 1) * j.nblk; ++cb) {
+      for (int cb = half; cb < C::kCtas * j.nblk; cb += 2) {
         uint32_t v0[32], v1[32];
+        __syncwarp();
         tmem_ld32(tz + cb * 64, v0);
         tmem_ld32(tz + cb * 64 + 32, v1);
         tmem_ld_wait();
         const int y = j.row0 + r0, x = j.n0 + cb * 64;
-        if (lane == 0) bulk_wait_read_all();
-        __syncwarp();
+        // Boxes that start past the tensor's end, and rows of dh behind the
+        // last, have nothing to write.
+        if (x >= a.D || (j.dw ? y >= a.V : j.m0 + r0 >= rows)) continue;
         if (j.dw) {
+          uint8_t* out = next_slot();
 #pragma unroll
           for (int ch = 0; ch < 8; ++ch) {
             const uint32_t* src = ch < 4 ? v0 + 8 * ch : v1 + 8 * (ch - 4);
@@ -468,56 +581,54 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               g[e] = f != 0.f ? dlref * __uint_as_float(src[e]) : 0.f;
-            *reinterpret_cast<uint4*>(rowp + ((ch ^ swz) << 4)) =
+            *reinterpret_cast<uint4*>(out + ((ch ^ swz) << 4)) =
                 make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]),
                            pack_bf16(g[6], g[7]));
           }
           fence_proxy_async_smem();
           __syncwarp();
-          // Boxes that start past the tensor's end have nothing to write.
-          if (lane == 0 && y < a.V && x < a.D) {
-            tma_store_2d(&tmDw, stage, x, y);
+          if (lane == 0) {
+            tma_store_2d(&tmDw, stage + slot * 4096, x, y);
             bulk_commit_group();
           }
         } else {
-          // fp32: two boxes of 32 columns, one after the other.
+          // fp32: two boxes of 32 columns.
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
+            if (x + 32 * i >= a.D) break;
             const uint32_t* v = i ? v1 : v0;
-            if (i) {
-              if (lane == 0) bulk_wait_read_all();
-              __syncwarp();
-            }
+            uint8_t* out = next_slot();
 #pragma unroll
             for (int ch = 0; ch < 8; ++ch)
-              *reinterpret_cast<uint4*>(rowp + ((ch ^ swz) << 4)) =
+              *reinterpret_cast<uint4*>(out + ((ch ^ swz) << 4)) =
                   make_uint4(v[4 * ch], v[4 * ch + 1], v[4 * ch + 2], v[4 * ch + 3]);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && x + 32 * i < a.D) {
+            if (lane == 0) {
               if (a.add)
-                tma_reduce_add_2d(&tmDh, stage, x + 32 * i, y);
+                tma_reduce_add_2d(&tmDh, stage + slot * 4096, x + 32 * i, y);
               else
-                tma_store_2d(&tmDh, stage, x + 32 * i, y);
+                tma_store_2d(&tmDh, stage + slot * 4096, x + 32 * i, y);
               bulk_commit_group();
             }
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc_empty + 8 * acc);
+      release(acc);
     }
-    if (kMode != kLse && lane == 0) bulk_wait_all();  // output stores complete
+    if (kMode == kGrad && lane == 0) bulk_wait_all();  // output stores complete
   }
 
   // Neither CTA leaves while the other may still signal its barriers.
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  if (kPair) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, kTmemCols);
+    if (kPair)
+      tmem_dealloc_pair(tmem, C::kTmem);
+    else
+      tmem_dealloc(tmem, C::kTmem);
   }
 }
 
@@ -526,38 +637,68 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct RowsArgs {
   int N, D, V;
   const int32_t* labels;
-  const uint16_t* h;
+  const uint16_t *h, *w;
+  const float* bias;    // or null
   const float* lse;     // backward
   const float* dloss;   // backward
   float *loss, *lse_out;  // forward: zeroed where there is no label
   Info* info;
   int *idx, *pos, *lab;
-  float *rlse, *dls;
+  float *rlse, *dls, *zl;
   uint16_t* hp;         // packed rows of h
 };
 
-constexpr int kRowsPerBlock = 256;
+constexpr int kRowsPerBlock = 32;
+constexpr int kRowsThreads = 256;
 
-// Block b packs rows 256 b .. 256 b + 255.  Each block reads all labels (and
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), s);
+    s = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), s);
+  }
+  return s;
+}
+
+// Block b takes rows 32 b .. 32 b + 31: it packs those that have a label and
+// computes their label's logit in fp32.  Each block reads all labels (and
 // dloss) to find how many rows with a label lie before its own, so one
 // launch does; labels are a few KB to a few hundred and come from L2.
 template <bool kBwd>
-__global__ void __launch_bounds__(kRowsPerBlock) rows_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
   __shared__ int cnt[3][8];
   __shared__ float mx[8];
-  __shared__ int dst[kRowsPerBlock];
+  __shared__ int dst[kRowsPerBlock], lab[kRowsPerBlock];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int base = blockIdx.x * kRowsPerBlock;
+  grid_launch_dependents();
   int total = 0, before = 0, bad = 0;
   float big = 0.f;
-  for (int i = tid; i < a.N; i += kRowsPerBlock) {
-    const int l = __ldg(a.labels + i);
-    if (l >= 0 && l < a.V) {
-      ++total;
-      before += i < base;
-      if (kBwd) big = fmaxf(big, fabsf(__ldg(a.dloss + i)));
+  for (int i0 = tid * 4; i0 < a.N; i0 += kRowsThreads * 4) {
+    int l[4] = {-1, -1, -1, -1};
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    if (i0 + 4 <= a.N) {
+      const int4 x = __ldg(reinterpret_cast<const int4*>(a.labels + i0));
+      l[0] = x.x; l[1] = x.y; l[2] = x.z; l[3] = x.w;
+      if (kBwd) {
+        const float4 y = __ldg(reinterpret_cast<const float4*>(a.dloss + i0));
+        d[0] = y.x; d[1] = y.y; d[2] = y.z; d[3] = y.w;
+      }
+    } else {
+      for (int e = 0; i0 + e < a.N; ++e) {
+        l[e] = __ldg(a.labels + i0 + e);
+        if (kBwd) d[e] = __ldg(a.dloss + i0 + e);
+      }
     }
-    bad |= l >= a.V;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool live = l[e] >= 0 && l[e] < a.V;
+      total += live;
+      before += live && i0 + e < base;
+      bad |= l[e] >= a.V;
+      if (kBwd && live) big = fmaxf(big, fabsf(d[e]));
+    }
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) {
@@ -582,87 +723,114 @@ __global__ void __launch_bounds__(kRowsPerBlock) rows_kernel(const RowsArgs a) {
     big = fmaxf(big, mx[w]);
   }
   const float dlref = big > 0.f && big < INFINITY ? big : 1.f;
-  __syncthreads();
-  const int n = base + tid;
-  const int l = n < a.N ? __ldg(a.labels + n) : -1;
-  const bool live = l >= 0 && l < a.V;
-  const unsigned m = __ballot_sync(0xffffffffu, live);
-  if (lane == 0) cnt[0][warp] = __popc(m);
-  __syncthreads();
-  int p = before + __popc(m & ((1u << lane) - 1));
-  for (int w = 0; w < warp; ++w) p += cnt[0][w];
-  dst[tid] = live ? p : -1;
-  if (live) {
-    a.idx[p] = n;
-    a.lab[p] = l;
-    if (kBwd) {
-      a.rlse[p] = __ldg(a.lse + n);
-      a.dls[p] = __ldg(a.dloss + n) / dlref;
+  if (warp == 0) {
+    const int n = base + lane;
+    const int l = n < a.N ? __ldg(a.labels + n) : -1;
+    const bool live = l >= 0 && l < a.V;
+    const unsigned m = __ballot_sync(0xffffffffu, live);
+    const int p = before + __popc(m & ((1u << lane) - 1));
+    dst[lane] = live ? p : -1;
+    lab[lane] = l;
+    if (live) {
+      a.idx[p] = n;
+      a.lab[p] = l;
+      if (kBwd) {
+        a.rlse[p] = __ldg(a.lse + n);
+        a.dls[p] = __ldg(a.dloss + n) / dlref;
+      }
+    }
+    if (n < a.N) {
+      if (kBwd) {
+        a.pos[n] = live ? p : -1;
+      } else if (!live) {
+        a.loss[n] = 0.f;
+        a.lse_out[n] = 0.f;
+      }
+    }
+    if (blockIdx.x == 0 && lane == 0) {
+      a.info->status = bad ? BB_ERR_BAD_LABEL : BB_OK;
+      a.info->rows = total;
+      a.info->direct = total == a.N;
+      a.info->dlref = dlref;
     }
   }
-  if (n < a.N) {
-    if (kBwd) {
-      a.pos[n] = live ? p : -1;
-    } else if (!live) {
-      a.loss[n] = 0.f;
-      a.lse_out[n] = 0.f;
-    }
-  }
-  if (blockIdx.x == 0 && tid == 0) {
-    a.info->status = bad ? BB_ERR_BAD_LABEL : BB_OK;
-    a.info->rows = total;
-    a.info->direct = total == a.N;
-    a.info->dlref = dlref;
-  }
-  if (total == a.N) return;
   __syncthreads();
   const int chunks = a.D / 8;  // 16-byte pieces of a row
+  const bool pack = total != a.N;
   for (int r = warp; r < kRowsPerBlock; r += 8) {
-    if (dst[r] < 0) continue;
+    const int p = dst[r];
+    if (p < 0) continue;
     const uint4* src = reinterpret_cast<const uint4*>(a.h + (size_t)(base + r) * a.D);
-    uint4* out = reinterpret_cast<uint4*>(a.hp + (size_t)dst[r] * a.D);
-    for (int c = lane; c < chunks; c += 32) out[c] = __ldg(src + c);
+    const uint4* wl = reinterpret_cast<const uint4*>(a.w + (size_t)lab[r] * a.D);
+    uint4* out = reinterpret_cast<uint4*>(a.hp + (size_t)p * a.D);
+    float s = 0.f;
+    for (int c0 = 0; c0 < chunks; c0 += 128) {
+      uint4 x[4], y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + 32 * i + lane < chunks) {
+          x[i] = __ldg(src + c0 + 32 * i + lane);
+          y[i] = __ldg(wl + c0 + 32 * i + lane);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + 32 * i + lane < chunks) {
+          s = dot8(x[i], y[i], s);
+          if (pack) out[c0 + 32 * i + lane] = x[i];
+        }
+    }
+#pragma unroll
+    for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+    if (lane == 0) a.zl[p] = s + (a.bias ? __ldg(a.bias + lab[r]) : 0.f);
   }
   // The rest of the last 64 packed rows, which dW's last K step reads, is
   // zero (times the zeros of dz).
-  if (blockIdx.x == 0) {
+  if (pack && blockIdx.x == 0) {
     const int end = (total + kBK - 1) / kBK * kBK;
     uint4* out = reinterpret_cast<uint4*>(a.hp);
-    for (size_t c = (size_t)total * chunks + tid; c < (size_t)end * chunks; c += kRowsPerBlock)
+    for (size_t c = (size_t)total * chunks + tid; c < (size_t)end * chunks; c += kRowsThreads)
       out[c] = make_uint4(0, 0, 0, 0);
   }
 }
 
-// Forward: merges the vocabulary half tiles' (max, sum) of 32 rows in a fixed
-// order: eight warps take every eighth tile, then their eight pairs.
+// Forward: merges the (max, sum) pairs of eight rows in a fixed order: 32
+// groups take every 32nd pair, then one warp's lanes their 32 results.
 __global__ void __launch_bounds__(256)
-    lse_merge_kernel(const Info* info, const float2* part, int vt, int Np, const float* zl,
+    lse_merge_kernel(const Info* info, const float2* part, int runs, int Np, const float* zl,
                      const int* idx, float* loss, float* lse) {
-  __shared__ float2 sh[8][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 32 + lane;
+  __shared__ float2 sh[8][33];
+  const int r = threadIdx.x & 7, g = threadIdx.x >> 3;
+  grid_wait();
   const int rows = info->rows;
-  if ((int)blockIdx.x * 32 >= rows) return;
+  if ((int)blockIdx.x * 8 >= rows) return;
+  const int row = blockIdx.x * 8 + r;
   float m = -INFINITY, s = 0.f;
-  for (int i = warp; i < vt; i += 8) {
+#pragma unroll 4
+  for (int i = g; i < runs; i += 32) {
     const float2 p = part[(size_t)i * Np + row];
     const float mm = fmaxf(m, p.x);
     const float ref = mm == -INFINITY ? 0.f : mm;
     s = s * ex2((m - ref) * kLog2e) + p.y * ex2((p.x - ref) * kLog2e);
     m = mm;
   }
-  sh[warp][lane] = make_float2(m, s);
+  sh[r][g] = make_float2(m, s);
   __syncthreads();
-  if (warp == 0 && row < rows) {
-    m = -INFINITY;
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, sh[w][lane].x);
-    const float ref = m == -INFINITY ? 0.f : m;
-    s = 0.f;
-    for (int w = 0; w < 8; ++w) s += sh[w][lane].y * ex2((sh[w][lane].x - ref) * kLog2e);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int out = blockIdx.x * 8 + warp;
+  if (out >= rows) return;
+  const float2 p = sh[warp][lane];
+  m = p.x;
+#pragma unroll
+  for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+  const float ref = m == -INFINITY ? 0.f : m;
+  s = p.y * ex2((p.x - ref) * kLog2e);
+#pragma unroll
+  for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+  if (lane == 0) {
     const float l = ref + logf(s);
-    const int n = idx[row];
+    const int n = idx[out];
     lse[n] = l;
-    loss[n] = l - zl[row];
+    loss[n] = l - zl[out];
   }
 }
 
@@ -674,12 +842,14 @@ __global__ void __launch_bounds__(256)
   const int chunks = D / 8;
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   const size_t n = i / chunks;
+  grid_wait();
   if (n >= (size_t)N) return;
   const int c = (int)(i % chunks) * 8;
   const int p = pos[n];
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (p >= 0) {
     const float dlref = info->dlref;
+#pragma unroll 4
     for (int s = 0; s < splits; ++s) {
       const float4* src = reinterpret_cast<const float4*>(acc + ((size_t)s * Np + p) * D + c);
       const float4 x = src[0], y = src[1];
@@ -697,8 +867,9 @@ __global__ void __launch_bounds__(256)
 // ---- host -------------------------------------------------------------------
 
 struct Plan {
-  int Np, pieces, Vp, splits, vt;
-  size_t idx, pos, lab, rlse, dls, hp, part, zl, dz, dh, dbp, total;  // byte offsets
+  bool pair;
+  int Np, a_rows, pieces, Vp, splits, runs;
+  size_t idx, pos, lab, rlse, dls, zl, hp, part, dz, dh, dbp, total;  // byte offsets
 };
 
 size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -707,24 +878,39 @@ int make_plan(int N, int D, int V, int pass, Plan* p) {
   if (N <= 0 || D <= 0 || V <= 0 || (pass != 0 && pass != 1)) return BB_ERR_INVALID;
   if (D % 8 != 0 || D < 64 || D > 65536 || N > (1 << 24) || V > (1 << 24))
     return BB_ERR_UNSUPPORTED;
-  p->Np = (int)up(N, kTM);
-  p->vt = (V + kTN - 1) / kTN;
-  if ((long long)(p->Np / kTM) * p->vt >= (1ll << 31)) return BB_ERR_UNSUPPORTED;
+  if ((long long)N * V >= (1ll << 44)) return BB_ERR_UNSUPPORTED;  // tile counts
+  p->pair = N > kBM;
+  const int tm = p->pair ? 2 * kBM : kBM;
+  p->Np = (int)up(N, tm);
+  // Few rows load a lower box of h; what the MMA reads below it reaches only
+  // accumulator rows that nothing uses.
+  p->a_rows = N < kBM ? (int)up(N, 8) : kBM;
+  // Pairs of (max, sum): per tile and epilogue warp, or per single CTA.
+  const int cols = p->pair ? Cfg<kLse, true>::kCols : Cfg<kLse, false>::kTN;
+  p->runs = (V + cols - 1) / cols;
+  if (!p->pair && p->runs > 148) p->runs = 148;
   // Pieces of equal size whose dz fits kPieceBytes (512 columns at least).
-  size_t cols = kPieceBytes / 2 / p->Np / kTN * kTN;
-  cols = cols < 512 ? 512 : cols;
-  p->pieces = (int)((V + cols - 1) / cols);
-  p->Vp = (int)up((V + p->pieces - 1) / p->pieces, kTN);
+  size_t fit = kPieceBytes / 2 / p->Np / 256 * 256;
+  fit = fit < 512 ? 512 : fit;
+  p->pieces = (int)((V + fit - 1) / fit);
+  p->Vp = (int)up((V + p->pieces - 1) / p->pieces, 256);
   p->pieces = (V + p->Vp - 1) / p->Vp;
-  // dh has few tiles of a long K when there are few rows: cut K so that a
-  // tile takes no more than half of a pair's share of the launch.
-  const long long dn = (D + kTN - 1) / kTN, mt = p->Np / kTM;
-  const long long hks = p->Vp / kBK, wks = (N + kBK - 1) / kBK;
-  const long long share = (mt * dn * hks + (long long)(p->Vp / kTM) * dn * wks) / (2 * 74);
-  const long long len = share < 8 ? 8 : share;
-  long long s = (hks + len - 1) / len;
-  p->splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
-  size_t off = 256;
+  // dh has few tiles of a long K when there are few rows: cut K into the
+  // fewest parts that keep a tile within a worker's share of the launch (each
+  // part writes dh's rows once more, and the last launch reads them).
+  const int workers = p->pair ? 74 : 148;
+  const long long dn = (D + 255) / 256, mt = p->Np / tm;
+  const long long nw = (p->Vp + tm - 1) / tm * dn, cw = tile_cost((N + kBK - 1) / kBK);
+  const int hks = p->Vp / kBK;
+  for (const int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+    if (s > 1 && hks / s < 4) break;
+    const long long nh = mt * dn * s, ch = tile_cost((hks + s - 1) / s);
+    p->splits = s;
+    if ((nh + workers - 1) / workers * ch <= (nh * ch + nw * cw) / workers) break;
+  }
+  // The status word is at the workspace's start; the rest begins at the next
+  // multiple of 256 bytes behind it (body()), so up to 512 bytes on.
+  size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = up(off + bytes, 256);
@@ -732,10 +918,11 @@ int make_plan(int N, int D, int V, int pass, Plan* p) {
   };
   p->idx = take((size_t)N * 4);
   p->lab = take((size_t)N * 4);
+  p->zl = take((size_t)N * 4);
   p->hp = take((size_t)p->Np * D * 2);
   if (pass == 0) {
-    p->part = take((size_t)2 * p->vt * p->Np * 8);
-    p->zl = take((size_t)N * 4);
+    // Whole tiles write their runs, past V too.
+    p->part = take(((size_t)p->runs + 4) * p->Np * 8);
   } else {
     p->pos = take((size_t)N * 4);
     p->rlse = take((size_t)N * 4);
@@ -744,38 +931,70 @@ int make_plan(int N, int D, int V, int pass, Plan* p) {
     p->dh = take((size_t)p->splits * p->Np * D * 4);
     p->dbp = take((size_t)(p->Np / kBM) * p->Vp * 4);
   }
-  p->total = off;
+  p->total = off + 512;
   return BB_OK;
 }
 
-template <int kMode>
-cudaError_t launch_gemm(const CeArgs& a, int tiles, int sms, const CUtensorMap& h,
-                        const CUtensorMap& hp, const CUtensorMap& w, const CUtensorMap& dz,
-                        const CUtensorMap& dw, const CUtensorMap& dh, cudaStream_t s) {
-  const size_t smem = 1024 + kStages * kStageBytes + kStageOut;
-  cudaError_t e = cudaFuncSetAttribute(ce_gemm_kernel<kMode>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
+char* body(void* workspace) {
+  return reinterpret_cast<char*>(((uintptr_t)workspace + 511) & ~(uintptr_t)255);
+}
+
+// Launches that wait for the one in front on the device (grid_wait), so that
+// their setup runs under its end.
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, int threads, size_t smem,
+                           bool pair, cudaStream_t s, Args... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * (tiles < sms / 2 ? tiles : sms / 2));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ce_gemm_kernel<kMode>, a, h, hp, w, dz, dw, dh);
+  cfg.attrs = attr;
+  cfg.numAttrs = pair ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int kMode, bool kPair>
+cudaError_t launch_gemm_as(const CeArgs& a, long long tiles, int sms, const CUtensorMap& h,
+                           const CUtensorMap& hp, const CUtensorMap& w, const CUtensorMap& dz,
+                           const CUtensorMap& dw, const CUtensorMap& dh, cudaStream_t s) {
+  using C = Cfg<kMode, kPair>;
+  const cudaError_t e = cudaFuncSetAttribute(ce_gemm_kernel<kMode, kPair>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int workers = sms / C::kCtas;
+  return launch_chained(ce_gemm_kernel<kMode, kPair>,
+                        C::kCtas * (unsigned)(tiles < workers ? tiles : workers), C::kThreads,
+                        C::kSmem, kPair, s, a, h, hp, w, dz, dw, dh);
+}
+
+template <int kMode>
+cudaError_t launch_gemm(const Plan& p, const CeArgs& a, int sms, const CUtensorMap& h,
+                        const CUtensorMap& hp, const CUtensorMap& w, const CUtensorMap& dz,
+                        const CUtensorMap& dw, const CUtensorMap& dh, cudaStream_t s) {
+  const int tm = p.pair ? 2 * kBM : kBM;
+  const int tn = p.pair ? Cfg<kMode, true>::kTN : Cfg<kMode, false>::kTN;
+  const long long mt = p.Np / tm, dn = (a.D + tn - 1) / tn;
+  const long long tiles = kMode == kGrad
+                              ? mt * dn * p.splits + (a.vn + tm - 1) / tm * dn
+                              : mt * ((a.vn + tn - 1) / tn);
+  return p.pair ? launch_gemm_as<kMode, true>(a, tiles, sms, h, hp, w, dz, dw, dh, s)
+                : launch_gemm_as<kMode, false>(a, tiles, sms, h, hp, w, dz, dw, dh, s);
 }
 
 int sm_count() {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
+  return sms < 148 ? sms : 148;  // the plan sizes by a B200's 148
 }
 
 }  // namespace
@@ -804,12 +1023,12 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
   for (const void* x : ptrs)
     if (!aligned16(x)) return BB_ERR_INVALID;
   if (!workspace || workspace_bytes < p.total) return BB_ERR_WORKSPACE;
-  char* ws = static_cast<char*>(workspace);
+  char* ws = body(workspace);
   cudaStream_t s = (cudaStream_t)stream;
   CUtensorMap tmH, tmHp, tmW;
-  if (!encode_bf16_2d(&tmH, h, hidden, N, hidden, 64, kBM) ||
-      !encode_bf16_2d(&tmHp, ws + p.hp, hidden, p.Np, hidden, 64, kBM) ||
-      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, 128))
+  if (!encode_bf16_2d(&tmH, h, hidden, N, hidden, 64, p.a_rows) ||
+      !encode_bf16_2d(&tmHp, ws + p.hp, hidden, p.Np, hidden, 64, p.a_rows) ||
+      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, p.pair ? 128 : 64))
     return BB_ERR_CUDA;
   RowsArgs r{};
   r.N = N;
@@ -817,13 +1036,16 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
   r.V = V;
   r.labels = labels;
   r.h = static_cast<const uint16_t*>(h);
+  r.w = static_cast<const uint16_t*>(w);
+  r.bias = bias;
+  r.zl = reinterpret_cast<float*>(ws + p.zl);
   r.loss = loss;
   r.lse_out = lse;
-  r.info = reinterpret_cast<Info*>(ws);
+  r.info = static_cast<Info*>(workspace);
   r.idx = reinterpret_cast<int*>(ws + p.idx);
   r.lab = reinterpret_cast<int*>(ws + p.lab);
   r.hp = reinterpret_cast<uint16_t*>(ws + p.hp);
-  rows_kernel<false><<<(N + kRowsPerBlock - 1) / kRowsPerBlock, kRowsPerBlock, 0, s>>>(r);
+  rows_kernel<false><<<(N + kRowsPerBlock - 1) / kRowsPerBlock, kRowsThreads, 0, s>>>(r);
   if (cudaGetLastError() != cudaSuccess) return BB_ERR_CUDA;
   CeArgs a{};
   a.N = N;
@@ -831,17 +1053,20 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
   a.V = V;
   a.Np = p.Np;
   a.vn = V;
+  a.a_bytes = p.a_rows * 2 * kBK;
   a.info = r.info;
   a.bias = bias;
   a.lab = r.lab;
   a.part = reinterpret_cast<float2*>(ws + p.part);
-  a.zl = reinterpret_cast<float*>(ws + p.zl);
-  if (launch_gemm<kLse>(a, p.Np / kTM * p.vt, sm_count(), tmH, tmHp, tmW, tmW, tmW, tmW, s) !=
-      cudaSuccess)
+  a.zl = r.zl;
+  const int sms = sm_count();
+  if (!p.pair && p.runs > sms) p.runs = sms;
+  if (launch_gemm<kLse>(p, a, sms, tmH, tmHp, tmW, tmW, tmW, tmW, s) != cudaSuccess ||
+      launch_chained(lse_merge_kernel, (N + 7) / 8, 256, 0, false, s, (const Info*)a.info,
+                     (const float2*)a.part, p.runs, p.Np, (const float*)r.zl, (const int*)r.idx,
+                     loss, lse) != cudaSuccess)
     return BB_ERR_CUDA;
-  lse_merge_kernel<<<(N + 31) / 32, 256, 0, s>>>(a.info, a.part, (V + kHalf - 1) / kHalf, p.Np, a.zl, r.idx, loss,
-                                                 lse);
-  return cudaGetLastError() == cudaSuccess ? BB_OK : BB_ERR_CUDA;
+  return BB_OK;
 }
 
 int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, const float* bias,
@@ -856,17 +1081,16 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   for (const void* x : ptrs)
     if (!aligned16(x)) return BB_ERR_INVALID;
   if (!workspace || workspace_bytes < p.total) return BB_ERR_WORKSPACE;
-  char* ws = static_cast<char*>(workspace);
+  char* ws = body(workspace);
   cudaStream_t s = (cudaStream_t)stream;
-  CUtensorMap tmH, tmHp, tmW, tmH64, tmHp64, tmW64, tmDz32, tmDz64, tmDw, tmDh;
-  if (!encode_bf16_2d(&tmH, h, hidden, N, hidden, 64, kBM) ||
-      !encode_bf16_2d(&tmHp, ws + p.hp, hidden, p.Np, hidden, 64, kBM) ||
-      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, 128) ||
+  CUtensorMap tmH, tmHp, tmW, tmH64, tmHp64, tmW64, tmDz, tmDw, tmDh;
+  if (!encode_bf16_2d(&tmH, h, hidden, N, hidden, 64, p.a_rows) ||
+      !encode_bf16_2d(&tmHp, ws + p.hp, hidden, p.Np, hidden, 64, p.a_rows) ||
+      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, p.pair ? 128 : 64) ||
       !encode_bf16_2d(&tmH64, h, hidden, N, hidden, 64, 64) ||
       !encode_bf16_2d(&tmHp64, ws + p.hp, hidden, p.Np, hidden, 64, 64) ||
       !encode_bf16_2d(&tmW64, w, hidden, V, hidden, 64, 64) ||
-      !encode_bf16_2d(&tmDz32, ws + p.dz, p.Vp, p.Np, p.Vp, 64, 32) ||
-      !encode_bf16_2d(&tmDz64, ws + p.dz, p.Vp, p.Np, p.Vp, 64, 64) ||
+      !encode_bf16_2d(&tmDz, ws + p.dz, 64, (uint64_t)p.Vp / 64 * p.Np, 64, 64, 64) ||
       !encode_bf16_2d(&tmDw, dw, hidden, V, hidden, 64, 32) ||
       !encode_f32_2d(&tmDh, ws + p.dh, hidden, (uint64_t)p.splits * p.Np, hidden, 32, 32))
     return BB_ERR_CUDA;
@@ -876,16 +1100,19 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   r.V = V;
   r.labels = labels;
   r.h = static_cast<const uint16_t*>(h);
+  r.w = static_cast<const uint16_t*>(w);
+  r.bias = bias;
+  r.zl = reinterpret_cast<float*>(ws + p.zl);
   r.lse = lse;
   r.dloss = dloss;
-  r.info = reinterpret_cast<Info*>(ws);
+  r.info = static_cast<Info*>(workspace);
   r.idx = reinterpret_cast<int*>(ws + p.idx);
   r.pos = reinterpret_cast<int*>(ws + p.pos);
   r.lab = reinterpret_cast<int*>(ws + p.lab);
   r.rlse = reinterpret_cast<float*>(ws + p.rlse);
   r.dls = reinterpret_cast<float*>(ws + p.dls);
   r.hp = reinterpret_cast<uint16_t*>(ws + p.hp);
-  rows_kernel<true><<<(N + kRowsPerBlock - 1) / kRowsPerBlock, kRowsPerBlock, 0, s>>>(r);
+  rows_kernel<true><<<(N + kRowsPerBlock - 1) / kRowsPerBlock, kRowsThreads, 0, s>>>(r);
   if (cudaGetLastError() != cudaSuccess) return BB_ERR_CUDA;
   CeArgs a{};
   a.N = N;
@@ -894,28 +1121,30 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   a.Np = p.Np;
   a.Vp = p.Vp;
   a.splits = p.splits;
+  a.a_bytes = p.a_rows * 2 * kBK;
   a.info = r.info;
   a.bias = bias;
   a.lab = r.lab;
   a.rlse = r.rlse;
   a.dls = r.dls;
+  a.zl = r.zl;
+  a.dz = reinterpret_cast<uint16_t*>(ws + p.dz);
   a.dbp = dbias ? reinterpret_cast<float*>(ws + p.dbp) : nullptr;
   a.dbias = dbias;
-  const int sms = sm_count(), mt = p.Np / kTM, dn = (hidden + kTN - 1) / kTN;
+  const int sms = sm_count();
   for (int i = 0; i < p.pieces; ++i) {
     a.v0 = i * p.Vp;
     a.vn = V - a.v0 < p.Vp ? V - a.v0 : p.Vp;
     a.add = i > 0;
-    const int nt = (a.vn + kTN - 1) / kTN, wm = (a.vn + kTM - 1) / kTM;
-    if (launch_gemm<kDz>(a, mt * nt, sms, tmH, tmHp, tmW, tmDz32, tmW, tmW, s) != cudaSuccess ||
-        launch_gemm<kGrad>(a, mt * dn * p.splits + wm * dn, sms, tmH64, tmHp64, tmW64, tmDz64,
-                           tmDw, tmDh, s) != cudaSuccess)
+    if (launch_gemm<kDz>(p, a, sms, tmH, tmHp, tmW, tmW, tmW, tmW, s) != cudaSuccess ||
+        launch_gemm<kGrad>(p, a, sms, tmH64, tmHp64, tmW64, tmDz, tmDw, tmDh, s) != cudaSuccess)
       return BB_ERR_CUDA;
   }
-  dh_round_kernel<<<(unsigned)(((size_t)N * (hidden / 8) + 255) / 256), 256, 0, s>>>(
-      a.info, N, hidden, p.Np, p.splits, r.pos, reinterpret_cast<float*>(ws + p.dh),
-      static_cast<uint16_t*>(dh));
-  return cudaGetLastError() == cudaSuccess ? BB_OK : BB_ERR_CUDA;
+  if (launch_chained(dh_round_kernel, (unsigned)(((size_t)N * (hidden / 8) + 255) / 256), 256, 0,
+                     false, s, (const Info*)a.info, N, hidden, p.Np, p.splits, (const int*)r.pos,
+                     (const float*)(ws + p.dh), static_cast<uint16_t*>(dh)) != cudaSuccess)
+    return BB_ERR_CUDA;
+  return BB_OK;
 }
 
 }  // extern "C"
