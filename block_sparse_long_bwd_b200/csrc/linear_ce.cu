@@ -62,7 +62,8 @@ struct Cfg {
   static constexpr uint32_t kOut = kEpi * kSlots * 4096;   // 32 x 128 B staging blocks
   static constexpr uint32_t kSmem = 1024 + kStages * kStage + kOut;
   static constexpr int kThreads = 64 + 32 * kEpi;
-  static constexpr uint32_t kTmem = 2 * kTN;               // columns: two accumulators
+  static constexpr int kAccs = 1;
+  static constexpr uint32_t kTmem = 2 * kTN * kAccs;       // columns, two tiles
 };
 
 // Cost of a gradient tile in K steps: a short one waits for its loads and
@@ -360,13 +361,13 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ---------------- MMA issue (one thread of rank 0) ----------------
+    // ---------------- MMA issue (rank 0) ----------------
     uint32_t it = 0, tc = 0;
     bool ok = rank == 0;
     for (int t; ok && (t = work.tile(tc)) >= 0; ++tc) {
       const Job j = work.job(a, t);
       const int acc = tc & 1;
-      if (!mbar_wait(&bars.acc_empty[acc], ((tc >> 1) & 1) ^ 1, &abort_flag, status)) break;
+      if (!mbar_wait_warp(&bars.acc_empty[acc], ((tc >> 1) & 1) ^ 1, &abort_flag, status)) break;
       tc_fence_after();
       // K-major tiles step 32 bytes per 16 of K; MN-major ones 16 rows of 128.
       const uint32_t a_mn = kMode == kGrad && j.dw, b_mn = kMode == kGrad;
@@ -375,38 +376,21 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
       const uint32_t albo = a_mn ? kBox : 16, blbo = b_mn ? kBox : 16;
       for (int ks = 0; ks < j.ksteps; ++ks, ++it) {
         const uint32_t st = it % C::kStages;
-        if (!mbar_wait(&bars.full[st], (it / C::kStages) & 1, &abort_flag, status)) {
+        if (!mbar_wait_warp(&bars.full[st], (it / C::kStages) & 1, &abort_flag, status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t aaddr = smem_u32(stages + st * C::kStage);
-          const uint32_t baddr = aaddr + kATile;
+        const uint32_t aaddr = smem_u32(stages + st * C::kStage);
+        const uint32_t baddr = aaddr + kATile;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t da = sdesc_sw128(aaddr + kk * astep, albo);
-            const uint64_t db = sdesc_sw128(baddr + kk * bstep, blbo);
-            const uint32_t more = (ks > 0 || kk > 0) ? 1u : 0u;
-            if (kPair)
-              mma_ss_pair(tmem + acc * C::kTN, da, db, idesc, more);
-            else
-              mma_ss(tmem + acc * C::kTN, da, db, idesc, more);
-          }
-          if (kPair)
-            mma_commit_pair(&bars.empty[st]);
-          else
-            mma_commit(&bars.empty[st]);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ss_warp(kPair, tmem + (acc * C::kAccs + (C::kAccs == 1 ? 0 : kk)) * C::kTN,
+                      sdesc_sw128(aaddr + kk * astep, albo), sdesc_sw128(baddr + kk * bstep, blbo),
+                      idesc, (ks > 0 || (C::kAccs == 1 && kk > 0)) ? 1u : 0u);
+        mma_commit_warp(kPair, &bars.empty[st]);
       }
-      if (ok && lane == 0) {
-        if (kPair)
-          mma_commit_pair(&bars.acc_full[acc]);
-        else
-          mma_commit(&bars.acc_full[acc]);
-      }
-      __syncwarp();
+      if (ok) mma_commit_warp(kPair, &bars.acc_full[acc]);
     }
   } else {
     // ------- epilogue (32 rows and, of eight warps, half of the columns each) -------
@@ -460,9 +444,9 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
         for (int i = 0; i < C::kCols / 32; ++i) bias_sh[warp - 2][32 * i + lane] = b[i];
         __syncwarp();
       }
-      if (!mbar_wait(&bars.acc_full[acc], (tc >> 1) & 1, &abort_flag, status)) break;
+      if (!mbar_wait_warp(&bars.acc_full[acc], (tc >> 1) & 1, &abort_flag, status)) break;
       tc_fence_after();
-      const uint32_t tz = tmem + acc * C::kTN + lane_off;
+      const uint32_t tz = tmem + acc * C::kAccs * C::kTN + lane_off;
       if (kMode != kGrad) {
         // Single CTAs see the same rows in every tile: one pair runs through.
         if (kPair) {
@@ -477,6 +461,15 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
           float2 z[16];
           tmem_ld_wait();
           add_bias(v, bias_sh[warp - 2] + c, z);
+#pragma unroll
+          for (int i = 1; i < C::kAccs; ++i) {
+            tmem_ld32(tz + i * C::kTN + cbeg + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              z[e] = add2(z[e], make_float2(__uint_as_float(v[2 * e]),
+                                            __uint_as_float(v[2 * e + 1])));
+          }
           if (c + 32 < C::kCols) tmem_ld32(tz + cbeg + c + 32, v);
           // The label's column of these 32.  Its logit is the one that
           // rows_kernel summed in fp32: the tensor core truncates its running
@@ -536,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
         } else if (a.dbp) {
           // Column sums of the CTA's 128 rows: the four quarters' sums in order.
           if (lane == 0) mbar_arrive_release(&bars.red);
-          if (!mbar_wait(&bars.red, tc & 1, &abort_flag, status)) break;
+          if (!mbar_wait_warp(&bars.red, tc & 1, &abort_flag, status)) break;
           for (int c = (warp - 2) * 32 + lane; c < C::kTN; c += 32 * C::kEpi)
             a.dbp[(size_t)(j.m0 / kBM + rank) * a.Vp + j.n0 + c] =
                 red[acc][0][c] + red[acc][1][c] + red[acc][2][c] + red[acc][3][c];
