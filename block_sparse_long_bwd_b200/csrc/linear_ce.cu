@@ -38,6 +38,7 @@ using namespace sm100;
 constexpr int kBM = 128, kBK = 64;             // rows of a CTA's tile, K step
 constexpr uint32_t kBox = 64 * 64 * 2;         // one 64 x 64 bf16 box: 8 KB
 constexpr uint32_t kATile = kBM * kBK * 2;     // 16 KB
+constexpr int kResA = 5;                       // A stages beside a resident B (below)
 constexpr size_t kPieceBytes = 256u << 20;     // dz of one vocabulary piece
 
 enum Mode { kLse = 0, kDz = 1, kGrad = 2 };
@@ -45,30 +46,31 @@ enum Mode { kLse = 0, kDz = 1, kGrad = 2 };
 // Tile shapes.  Pairs of CTAs (cta_group::2) form 256 x 256 tiles: 128 rows of
 // A and 128 columns of B in each CTA's shared memory.  Up to 128 rows a pair's
 // second half would be empty, and the vocabulary's weights bound the launch:
-// single CTAs take 128 x 64 logits (enough tiles to keep every SM loading)
-// and 128 x 256 gradients.  Two accumulators, so that a tile's epilogue runs
+// single CTAs take 128 x 128 logits (enough tiles to keep every SM loading)
+// and 128 x 256 gradients.  There a dW tile's B, up to 128 rows of 256 columns
+// of h, is the same for every tile of those columns: it stays in shared
+// memory while the CTA walks down the words, and the freed stages hold A's.  Two accumulators, so that a tile's epilogue runs
 // under the next one's MMAs.
 template <int kMode, bool kPair>
 struct Cfg {
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kTM = kBM * kCtas;
-  static constexpr int kTN = kPair || kMode == kGrad ? 256 : 64;
-  static constexpr int kEpi = kTN == 256 ? 8 : 4;          // epilogue warps
+  static constexpr int kTN = kPair || kMode == kGrad ? 256 : 128;
+  static constexpr int kEpi = 8;                           // epilogue warps
   static constexpr int kCols = kTN / (kEpi / 4);           // columns of one (logits)
-  static constexpr int kSlots = kMode == kGrad ? 2 : 0;
+  static constexpr int kSlots = kMode == kGrad ? 2 : 0;    // staging blocks of one
   static constexpr uint32_t kBTile = kTN / kCtas * kBK * 2;
   static constexpr uint32_t kStage = kATile + kBTile;
-  static constexpr int kStages = kPair ? 5 : kMode == kGrad ? 3 : 8;
+  static constexpr int kStages = kPair ? 5 : kMode == kGrad ? 3 : 6;
   static constexpr uint32_t kOut = kEpi * kSlots * 4096;   // 32 x 128 B staging blocks
   static constexpr uint32_t kSmem = 1024 + kStages * kStage + kOut;
   static constexpr int kThreads = 64 + 32 * kEpi;
-  static constexpr int kAccs = 1;
-  static constexpr uint32_t kTmem = 2 * kTN * kAccs;       // columns, two tiles
+  static constexpr uint32_t kTmem = 2 * kTN;               // columns: two accumulators
 };
 
-// Cost of a gradient tile in K steps: a short one waits for its loads and
-// stores instead.
-__host__ __device__ constexpr int tile_cost(int ksteps) { return ksteps < 3 ? 3 : ksteps; }
+// Cost of a gradient tile in K steps: a short one takes as long as its
+// epilogue, measured as four.
+__host__ __device__ constexpr int tile_cost(int ksteps) { return ksteps < 4 ? 4 : ksteps; }
 
 // What rows_kernel finds out on the device, at the workspace's start.
 struct Info {
@@ -100,7 +102,8 @@ struct CeArgs {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], acc_full[2], acc_empty[2], red;
+  uint64_t full[6], empty[6], acc_full[2], acc_empty[2], red;
+  uint64_t a_full[kResA], a_empty[kResA], b_full;  // dW of a single CTA
 };
 
 // One output tile.
@@ -118,13 +121,17 @@ struct Job {
 // costs, dh's (K: the piece's columns, cut into `splits`) and dW's (K: the
 // rows).  The dearer kind is dealt out first; workers that got one fewer of
 // it take `lead` more of the cheaper kind before that is dealt out to all, so
-// the workers end within about one cheap tile of each other.
+// the workers end within about one cheap tile of each other.  Single CTAs take
+// their tiles of dh, then a run of dW's tiles, ordered by columns first so that
+// h's part is loaded once or twice; the runs are cut by the tiles' columns
+// (the last may have few) less what the tiles of dh cost.
 template <int kMode, bool kPair>
 struct Work {
   using C = Cfg<kMode, kPair>;
   int w, stride;                  // this worker, workers
   int tiles, mt, dn, hks, wks;
   int dw_first, na, nb, more, lead;  // kinds in order; workers with one more of the first
+  int wm, dw0, dw1;                  // single CTAs: row tiles of dW; this one's run
   __device__ __forceinline__ Work(const CeArgs& a, int rows, int worker, int workers)
       : w(worker), stride(workers) {
     mt = (rows + C::kTM - 1) / C::kTM;
@@ -137,6 +144,31 @@ struct Work {
     wks = (rows + kBK - 1) / kBK;
     const int nh = mt * dn * a.splits, nw = (a.vn + C::kTM - 1) / C::kTM * dn;
     const int ch = tile_cost(hks / a.splits), cw = tile_cost(wks);
+    if (!kPair) {
+      dw_first = 0;
+      na = nh;
+      wm = nw / dn;
+      const int cols = (a.D + 63) / 64;  // 64-column blocks of dW's rows
+      more = nh % stride;
+      // Shares in units of a 64-column block, a tile being its blocks and one
+      // for itself: x for the workers with one tile of dh more, x + d for the
+      // others.
+      const float d = more ? 5.f * ch / cw : 0.f, all = (float)wm * (cols + dn);
+      float x = (all - d * (stride - more)) / stride, y = x + d;
+      if (x < 0.f) {
+        x = 0.f;
+        y = all / (stride - more);
+      }
+      auto start = [&](int w) {  // first tile of worker w
+        const float b = w >= stride ? all : w <= more ? w * x : more * x + (w - more) * y;
+        const int n = min((int)(b / (5.f * wm)), dn - 1), blk = min(4, cols - 4 * n) + 1;
+        const int m = (int)((b - 5.f * n * wm) / blk + 0.5f);
+        return n * wm + min(m, wm);
+      };
+      dw0 = start(w);
+      dw1 = w + 1 >= stride ? wm * dn : start(w + 1);
+      return;
+    }
     dw_first = cw > ch;
     na = dw_first ? nw : nh;
     nb = dw_first ? nh : nw;
@@ -154,6 +186,7 @@ struct Work {
     const int mine = na / stride + (w < more);
     if (i < mine) return i * stride + w;
     i -= mine;
+    if (!kPair) return dw0 + i < dw1 ? na + dw0 + i : -1;
     int u;
     if (w >= more) {
       if (i < lead) return na + i * (stride - more) + (w - more);
@@ -177,6 +210,7 @@ struct Work {
     }
     j.dw = dw_first ? t < na : t >= na;
     int u = t < na ? t : t - na;
+    if (!kPair && j.dw) u = u % wm * dn + u / wm;  // columns first
     j.n0 = (u % dn) * C::kTN;
     const int left = (a.D - j.n0 + 64 * C::kCtas - 1) / (64 * C::kCtas);
     j.nblk = left < j.nblk ? left : j.nblk;
@@ -278,6 +312,11 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
       mbar_init(&bars.acc_empty[s], C::kCtas * C::kEpi);
     }
     mbar_init(&bars.red, C::kEpi);
+    for (int s = 0; s < kResA; ++s) {
+      mbar_init(&bars.a_full[s], 1);
+      mbar_init(&bars.a_empty[s], 1);
+    }
+    mbar_init(&bars.b_full, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -301,25 +340,56 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
   const Work<kMode, kPair> work(a, rows, blockIdx.x / C::kCtas, gridDim.x / C::kCtas);
 
   if (warp == 0) {
-    // ---------------- TMA loads (one thread of each CTA) ----------------
-    if (lane == 0) {
-      uint32_t it = 0;
+    // ---------------- TMA loads ----------------
+    {
+      uint32_t it = 0, ia = 0;  // loads of the ring; of A beside a resident B
+      int n_res = -1;           // columns of the resident B
+      // dh of up to 64 rows: the lower half of A reaches no row that is used.
+      const int a_boxes = !kPair && rows <= 64 ? 1 : 2;
       bool ok = true;
+      auto load = [&](const uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+        tma_load_2d_warp(kPair, smem_u32(dst), map, kPair ? map_rank(bar, 0) : smem_u32(bar), x, y);
+      };
+      // Waits until the MMAs have released every stage loaded so far.
+      auto drained = [&]() {
+        bool done = true;
+        for (uint32_t q = it > C::kStages ? it - C::kStages : 0; q < it && done; ++q)
+          done = mbar_wait_warp(&bars.empty[q % C::kStages], (q / C::kStages) & 1, &abort_flag, status);
+        for (uint32_t q = ia > kResA ? ia - kResA : 0; q < ia && done; ++q)
+          done = mbar_wait_warp(&bars.a_empty[q % kResA], (q / kResA) & 1, &abort_flag, status);
+        return done;
+      };
       for (int i = 0, t; ok && (t = work.tile(i)) >= 0; ++i) {
         const Job j = work.job(a, t);
+        if (!kPair && kMode == kGrad && j.dw) {
+          if (n_res != j.n0 && j.ksteps > 0) {
+            // Every MMA on what the stages and the old B hold is done.
+            ok = drained();
+            if (!ok) break;
+            n_res = j.n0;
+            mbar_expect_tx_warp(&bars.b_full, j.ksteps * j.nblk * kBox);
+            for (int k = 0; k < j.ksteps; ++k)
+              for (int b = 0; b < j.nblk; ++b)
+                load(stages + (k * 4 + b) * kBox, mapH, &bars.b_full, j.n0 + 64 * b, k * kBK);
+          }
+          for (int k = 0; k < j.ksteps; ++k, ++ia) {
+            const uint32_t st = ia % kResA;
+            ok = mbar_wait_warp(&bars.a_empty[st], ((ia / kResA) & 1) ^ 1, &abort_flag, status);
+            if (!ok) break;
+            mbar_expect_tx_warp(&bars.a_full[st], kATile);
+            for (int b = 0; b < 2; ++b)
+              load(stages + 8 * kBox + st * kATile + b * kBox, &tmDz, &bars.a_full[st], 0,
+                   (j.m0 / 64 + b) * a.Np + k * kBK);
+          }
+          continue;
+        }
         // Single CTAs all read the same few rows of h: each tile begins at
         // another K step, or all would wait for the same lines of L2.
         const int k_first = !kPair && kMode != kGrad ? t % j.ksteps : 0;
         const int m0 = j.m0 + rank * kBM, n0 = j.n0 + rank * 64 * j.nblk;
-        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
-          if (kPair)
-            tma_load_2d_pair(dst, map, map_rank(bar, 0), x, y);
-          else
-            tma_load_2d(dst, map, bar, x, y);
-        };
         for (int ks = 0; ks < j.ksteps; ++ks, ++it) {
           const uint32_t st = it % C::kStages;
-          if (!mbar_wait(&bars.empty[st], ((it / C::kStages) & 1) ^ 1, &abort_flag, status)) {
+          if (!mbar_wait_warp(&bars.empty[st], ((it / C::kStages) & 1) ^ 1, &abort_flag, status)) {
             ok = false;
             break;
           }
@@ -327,7 +397,8 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
           uint8_t* pb = pa + kATile;
           uint64_t* bar = &bars.full[st];
           if (rank == 0)
-            mbar_expect_tx(bar, C::kCtas * ((kMode == kGrad ? kATile : a.a_bytes) + j.nblk * kBox));
+            mbar_expect_tx_warp(bar, C::kCtas * ((kMode == kGrad ? a_boxes * kBox : a.a_bytes) +
+                                                 j.nblk * kBox));
           const int kr = k_first + ks;
           const int k = (j.k0 + (kr < j.ksteps ? kr : kr - j.ksteps)) * kBK;
           if (kMode != kGrad) {
@@ -336,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
           } else {
             // dW: A = dz^T (columns of dz along M), B = h; dh: A = dz, B = W.
             // A 64 x 64 box of a panel of dz is 8 KB in one piece.
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < a_boxes; ++i)
               load(pa + i * kBox, &tmDz, bar, 0,
                    j.dw ? (m0 / 64 + i) * a.Np + k : k / 64 * a.Np + m0 + 64 * i);
             for (int i = 0; i < j.nblk; ++i)
@@ -345,8 +416,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
         }
       }
       // The last stages' releases reach this CTA before it may leave.
-      for (int i = 0; i < C::kStages && ok; ++i, ++it)
-        ok = mbar_wait(&bars.empty[it % C::kStages], ((it / C::kStages) & 1) ^ 1, &abort_flag, status);
+      if (ok) drained();
       if (abort_flag && rank == 0) {
         // Let issued copies (both CTAs') land before shared memory goes away;
         // rank 1 waits at the cluster barrier meanwhile.
@@ -358,11 +428,23 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
                    globaltimer() - t0 < 100000000ull) {
             }
           }
+        if (!kPair && kMode == kGrad) {
+          const uint64_t t0 = globaltimer();
+          for (uint32_t q = ia > kResA ? ia - kResA : 0; q < ia; ++q)
+            while (!mbar_try_wait(&bars.a_full[q % kResA], (q / kResA) & 1) &&
+                   globaltimer() - t0 < 100000000ull) {
+            }
+          // B's latest load: its phase is the number of columns taken so far,
+          // which this wait does not know; it gives the copy time to land.
+          while (n_res >= 0 && globaltimer() - t0 < 1000000ull) {
+          }
+        }
       }
     }
   } else if (warp == 1) {
     // ---------------- MMA issue (rank 0) ----------------
-    uint32_t it = 0, tc = 0;
+    uint32_t it = 0, tc = 0, ia = 0, ib = 0;
+    int n_res = -1;
     bool ok = rank == 0;
     for (int t; ok && (t = work.tile(tc)) >= 0; ++tc) {
       const Job j = work.job(a, t);
@@ -374,6 +456,29 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
       const uint32_t idesc = idesc_bf16(C::kTM, 64 * C::kCtas * j.nblk, a_mn, b_mn);
       const uint32_t astep = a_mn ? 2048 : 32, bstep = b_mn ? 2048 : 32;
       const uint32_t albo = a_mn ? kBox : 16, blbo = b_mn ? kBox : 16;
+      if (!kPair && kMode == kGrad && j.dw) {
+        if (n_res != j.n0 && j.ksteps > 0) {
+          ok = mbar_wait_warp(&bars.b_full, ib & 1, &abort_flag, status);
+          if (!ok) break;
+          n_res = j.n0;
+          ++ib;
+        }
+        for (int k = 0; k < j.ksteps; ++k, ++ia) {
+          const uint32_t st = ia % kResA;
+          ok = mbar_wait_warp(&bars.a_full[st], (ia / kResA) & 1, &abort_flag, status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t aaddr = smem_u32(stages + 8 * kBox + st * kATile);
+          const uint32_t baddr = smem_u32(stages + 4 * k * kBox);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss_warp(false, tmem + acc * C::kTN, sdesc_sw128(aaddr + kk * 2048, kBox),
+                        sdesc_sw128(baddr + kk * 2048, kBox), idesc, (k > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_warp(false, &bars.a_empty[st]);
+        }
+        if (ok) mma_commit_warp(false, &bars.acc_full[acc]);
+        continue;
+      }
       for (int ks = 0; ks < j.ksteps; ++ks, ++it) {
         const uint32_t st = it % C::kStages;
         if (!mbar_wait_warp(&bars.full[st], (it / C::kStages) & 1, &abort_flag, status)) {
@@ -385,9 +490,9 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
         const uint32_t baddr = aaddr + kATile;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ss_warp(kPair, tmem + (acc * C::kAccs + (C::kAccs == 1 ? 0 : kk)) * C::kTN,
-                      sdesc_sw128(aaddr + kk * astep, albo), sdesc_sw128(baddr + kk * bstep, blbo),
-                      idesc, (ks > 0 || (C::kAccs == 1 && kk > 0)) ? 1u : 0u);
+          mma_ss_warp(kPair, tmem + acc * C::kTN, sdesc_sw128(aaddr + kk * astep, albo),
+                      sdesc_sw128(baddr + kk * bstep, blbo), idesc,
+                      (ks > 0 || kk > 0) ? 1u : 0u);
         mma_commit_warp(kPair, &bars.empty[st]);
       }
       if (ok) mma_commit_warp(kPair, &bars.acc_full[acc]);
@@ -446,7 +551,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
       }
       if (!mbar_wait_warp(&bars.acc_full[acc], (tc >> 1) & 1, &abort_flag, status)) break;
       tc_fence_after();
-      const uint32_t tz = tmem + acc * C::kAccs * C::kTN + lane_off;
+      const uint32_t tz = tmem + acc * C::kTN + lane_off;
       if (kMode != kGrad) {
         // Single CTAs see the same rows in every tile: one pair runs through.
         if (kPair) {
@@ -456,20 +561,11 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
         uint32_t v[32];
         __syncwarp();
         tmem_ld32(tz + cbeg, v);
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < C::kCols; c += 32) {
           float2 z[16];
           tmem_ld_wait();
           add_bias(v, bias_sh[warp - 2] + c, z);
-#pragma unroll
-          for (int i = 1; i < C::kAccs; ++i) {
-            tmem_ld32(tz + i * C::kTN + cbeg + c, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              z[e] = add2(z[e], make_float2(__uint_as_float(v[2 * e]),
-                                            __uint_as_float(v[2 * e + 1])));
-          }
           if (c + 32 < C::kCols) tmem_ld32(tz + cbeg + c + 32, v);
           // The label's column of these 32.  Its logit is the one that
           // rows_kernel summed in fp32: the tensor core truncates its running
@@ -525,7 +621,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
           if (kPair)
             a.part[(size_t)((j.n0 + cbeg) / C::kCols) * a.Np + row] = make_float2(m, s);
           else if (work.tile(tc + 1) < 0)
-            a.part[(size_t)work.w * a.Np + row] = make_float2(m, s);
+            a.part[(size_t)(2 * work.w + half) * a.Np + row] = make_float2(m, s);
         } else if (a.dbp) {
           // Column sums of the CTA's 128 rows: the four quarters' sums in order.
           if (lane == 0) mbar_arrive_release(&bars.red);
@@ -545,8 +641,6 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
         for (int m = 0; m < blocks; ++m) s += a.dbp[(size_t)m * a.Vp + v];
         if (a.v0 + v < a.V) a.dbias[a.v0 + v] = s * dlref;
       }
-      // A tile without K steps (no rows) is zero.
-      const float f = j.ksteps > 0 ? 1.f : 0.f;
       // The next staging slot, once the store before last has read it.
       auto next_slot = [&]() {
         slot ^= 1;
@@ -561,6 +655,10 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
         tmem_ld32(tz + cb * 64, v0);
         tmem_ld32(tz + cb * 64 + 32, v1);
         tmem_ld_wait();
+        if (j.ksteps == 0) {  // no rows at all: zero, whatever the accumulator holds
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v0[e] = v1[e] = 0u;
+        }
         const int y = j.row0 + r0, x = j.n0 + cb * 64;
         // Boxes that start past the tensor's end, and rows of dh behind the
         // last, have nothing to write.
@@ -570,13 +668,16 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
 #pragma unroll
           for (int ch = 0; ch < 8; ++ch) {
             const uint32_t* src = ch < 4 ? v0 + 8 * ch : v1 + 8 * (ch - 4);
-            float g[8];
+            uint32_t u[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              g[e] = f != 0.f ? dlref * __uint_as_float(src[e]) : 0.f;
+            for (int e = 0; e < 4; ++e) {
+              const float2 g = mul2(make_float2(__uint_as_float(src[2 * e]),
+                                                __uint_as_float(src[2 * e + 1])),
+                                    make_float2(dlref, dlref));
+              u[e] = pack_bf16(g.x, g.y);
+            }
             *reinterpret_cast<uint4*>(out + ((ch ^ swz) << 4)) =
-                make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]),
-                           pack_bf16(g[6], g[7]));
+                make_uint4(u[0], u[1], u[2], u[3]);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -629,6 +730,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
 
 struct RowsArgs {
   int N, D, V;
+  int per_block;        // rows of a block
   const int32_t* labels;
   const uint16_t *h, *w;
   const float* bias;    // or null
@@ -641,7 +743,7 @@ struct RowsArgs {
   uint16_t* hp;         // packed rows of h
 };
 
-constexpr int kRowsPerBlock = 32;
+constexpr int kRowsPerBlock = 32;  // at most
 constexpr int kRowsThreads = 256;
 
 __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
@@ -654,7 +756,8 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
   return s;
 }
 
-// Block b takes rows 32 b .. 32 b + 31: it packs those that have a label and
+// Block b takes per_block rows (8 of up to 1024 rows, one per warp; 32 of
+// more, so that fewer blocks read the labels): it packs those that have a label and
 // computes their label's logit in fp32.  Each block reads all labels (and
 // dloss) to find how many rows with a label lie before its own, so one
 // launch does; labels are a few KB to a few hundred and come from L2.
@@ -664,7 +767,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
   __shared__ float mx[8];
   __shared__ int dst[kRowsPerBlock], lab[kRowsPerBlock];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int base = blockIdx.x * kRowsPerBlock;
+  const int base = blockIdx.x * a.per_block;
   grid_launch_dependents();
   int total = 0, before = 0, bad = 0;
   float big = 0.f;
@@ -717,7 +820,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
   }
   const float dlref = big > 0.f && big < INFINITY ? big : 1.f;
   if (warp == 0) {
-    const int n = base + lane;
+    const int n = lane < a.per_block ? base + lane : a.N;
     const int l = n < a.N ? __ldg(a.labels + n) : -1;
     const bool live = l >= 0 && l < a.V;
     const unsigned m = __ballot_sync(0xffffffffu, live);
@@ -750,7 +853,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
   __syncthreads();
   const int chunks = a.D / 8;  // 16-byte pieces of a row
   const bool pack = total != a.N;
-  for (int r = warp; r < kRowsPerBlock; r += 8) {
+  for (int r = warp; r < a.per_block; r += 8) {
     const int p = dst[r];
     if (p < 0) continue;
     const uint4* src = reinterpret_cast<const uint4*>(a.h + (size_t)(base + r) * a.D);
@@ -828,27 +931,45 @@ __global__ void __launch_bounds__(256)
 }
 
 // Backward's end: dh rows rounded from the fp32 sums (0 where there is no
-// label), eight columns per thread.
+// label).  A block takes 256 / kGroups pieces of eight columns; with several
+// parts per sum, kGroups threads share a piece's parts and their sums are
+// added in order.
+template <int kGroups>
 __global__ void __launch_bounds__(256)
     dh_round_kernel(const Info* info, int N, int D, int Np, int splits, const int* pos,
                     const float* acc, uint16_t* dh) {
-  const int chunks = D / 8;
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  constexpr int kPieces = 256 / kGroups;
+  __shared__ float sh[kGroups > 1 ? kGroups : 1][kPieces][kGroups > 1 ? 9 : 1];
+  const int chunks = D / 8, piece = threadIdx.x % kPieces, g = threadIdx.x / kPieces;
+  const size_t i = (size_t)blockIdx.x * kPieces + piece;
   const size_t n = i / chunks;
-  grid_wait();
-  if (n >= (size_t)N) return;
+  const bool live = n < (size_t)N;
   const int c = (int)(i % chunks) * 8;
-  const int p = pos[n];
+  grid_wait();
+  const int p = live ? pos[n] : -1;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (p >= 0) {
-    const float dlref = info->dlref;
 #pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
+    for (int s = g; s < splits; s += kGroups) {
       const float4* src = reinterpret_cast<const float4*>(acc + ((size_t)s * Np + p) * D + c);
       const float4 x = src[0], y = src[1];
       v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
       v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
     }
+  }
+  if (kGroups > 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sh[g][piece][e] = v[e];
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int q = 1; q < kGroups; ++q)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += sh[q][piece][e];
+  }
+  if (!live) return;
+  if (p >= 0) {
+    const float dlref = info->dlref;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= dlref;
   }
@@ -878,10 +999,9 @@ int make_plan(int N, int D, int V, int pass, Plan* p) {
   // Few rows load a lower box of h; what the MMA reads below it reaches only
   // accumulator rows that nothing uses.
   p->a_rows = N < kBM ? (int)up(N, 8) : kBM;
-  // Pairs of (max, sum): per tile and epilogue warp, or per single CTA.
-  const int cols = p->pair ? Cfg<kLse, true>::kCols : Cfg<kLse, false>::kTN;
-  p->runs = (V + cols - 1) / cols;
-  if (!p->pair && p->runs > 148) p->runs = 148;
+  // Pairs of (max, sum): of every 128 columns, or two of a single CTA.
+  p->runs = (V + 127) / 128;
+  if (!p->pair) p->runs = 2 * (p->runs > 148 ? 148 : p->runs);
   // Pieces of equal size whose dz fits kPieceBytes (512 columns at least).
   size_t fit = kPieceBytes / 2 / p->Np / 256 * 256;
   fit = fit < 512 ? 512 : fit;
@@ -1021,10 +1141,11 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
   CUtensorMap tmH, tmHp, tmW;
   if (!encode_bf16_2d(&tmH, h, hidden, N, hidden, 64, p.a_rows) ||
       !encode_bf16_2d(&tmHp, ws + p.hp, hidden, p.Np, hidden, 64, p.a_rows) ||
-      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, p.pair ? 128 : 64))
+      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, 128))
     return BB_ERR_CUDA;
   RowsArgs r{};
   r.N = N;
+  r.per_block = N <= 1024 ? 8 : kRowsPerBlock;
   r.D = hidden;
   r.V = V;
   r.labels = labels;
@@ -1038,7 +1159,7 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
   r.idx = reinterpret_cast<int*>(ws + p.idx);
   r.lab = reinterpret_cast<int*>(ws + p.lab);
   r.hp = reinterpret_cast<uint16_t*>(ws + p.hp);
-  rows_kernel<false><<<(N + kRowsPerBlock - 1) / kRowsPerBlock, kRowsThreads, 0, s>>>(r);
+  rows_kernel<false><<<(N + r.per_block - 1) / r.per_block, kRowsThreads, 0, s>>>(r);
   if (cudaGetLastError() != cudaSuccess) return BB_ERR_CUDA;
   CeArgs a{};
   a.N = N;
@@ -1053,7 +1174,7 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
   a.part = reinterpret_cast<float2*>(ws + p.part);
   a.zl = r.zl;
   const int sms = sm_count();
-  if (!p.pair && p.runs > sms) p.runs = sms;
+  if (!p.pair && p.runs > 2 * sms) p.runs = 2 * sms;
   if (launch_gemm<kLse>(p, a, sms, tmH, tmHp, tmW, tmW, tmW, tmW, s) != cudaSuccess ||
       launch_chained(lse_merge_kernel, (N + 7) / 8, 256, 0, false, s, (const Info*)a.info,
                      (const float2*)a.part, p.runs, p.Np, (const float*)r.zl, (const int*)r.idx,
@@ -1079,7 +1200,7 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   CUtensorMap tmH, tmHp, tmW, tmH64, tmHp64, tmW64, tmDz, tmDw, tmDh;
   if (!encode_bf16_2d(&tmH, h, hidden, N, hidden, 64, p.a_rows) ||
       !encode_bf16_2d(&tmHp, ws + p.hp, hidden, p.Np, hidden, 64, p.a_rows) ||
-      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, p.pair ? 128 : 64) ||
+      !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, 128) ||
       !encode_bf16_2d(&tmH64, h, hidden, N, hidden, 64, 64) ||
       !encode_bf16_2d(&tmHp64, ws + p.hp, hidden, p.Np, hidden, 64, 64) ||
       !encode_bf16_2d(&tmW64, w, hidden, V, hidden, 64, 64) ||
@@ -1089,6 +1210,7 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
     return BB_ERR_CUDA;
   RowsArgs r{};
   r.N = N;
+  r.per_block = N <= 1024 ? 8 : kRowsPerBlock;
   r.D = hidden;
   r.V = V;
   r.labels = labels;
@@ -1105,7 +1227,7 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   r.rlse = reinterpret_cast<float*>(ws + p.rlse);
   r.dls = reinterpret_cast<float*>(ws + p.dls);
   r.hp = reinterpret_cast<uint16_t*>(ws + p.hp);
-  rows_kernel<true><<<(N + kRowsPerBlock - 1) / kRowsPerBlock, kRowsThreads, 0, s>>>(r);
+  rows_kernel<true><<<(N + r.per_block - 1) / r.per_block, kRowsThreads, 0, s>>>(r);
   if (cudaGetLastError() != cudaSuccess) return BB_ERR_CUDA;
   CeArgs a{};
   a.N = N;
@@ -1133,8 +1255,11 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
         launch_gemm<kGrad>(p, a, sms, tmH64, tmHp64, tmW64, tmDz, tmDw, tmDh, s) != cudaSuccess)
       return BB_ERR_CUDA;
   }
-  if (launch_chained(dh_round_kernel, (unsigned)(((size_t)N * (hidden / 8) + 255) / 256), 256, 0,
-                     false, s, (const Info*)a.info, N, hidden, p.Np, p.splits, (const int*)r.pos,
+  const size_t pieces = (size_t)N * (hidden / 8);
+  const int groups = p.splits > 4 ? 8 : 1;
+  if (launch_chained(groups > 1 ? dh_round_kernel<8> : dh_round_kernel<1>,
+                     (unsigned)((pieces * groups + 255) / 256), 256, 0, false, s,
+                     (const Info*)a.info, N, hidden, p.Np, p.splits, (const int*)r.pos,
                      (const float*)(ws + p.dh), static_cast<uint16_t*>(dh)) != cudaSuccess)
     return BB_ERR_CUDA;
   return BB_OK;
