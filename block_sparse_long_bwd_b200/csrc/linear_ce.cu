@@ -743,7 +743,7 @@ struct RowsArgs {
   uint16_t* hp;         // packed rows of h
 };
 
-constexpr int kRowsPerBlock = 32;  // at most
+constexpr int kRowsPerBlock = 32;  // at most; a lane of warp 0 each
 constexpr int kRowsThreads = 256;
 
 __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
@@ -765,36 +765,34 @@ template <bool kBwd>
 __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
   __shared__ int cnt[3][8];
   __shared__ float mx[8];
+  static_assert(kRowsPerBlock == 32, "one lane of a warp per row");
   __shared__ int dst[kRowsPerBlock], lab[kRowsPerBlock];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int base = blockIdx.x * a.per_block;
   grid_launch_dependents();
   int total = 0, before = 0, bad = 0;
   float big = 0.f;
-  for (int i0 = tid * 4; i0 < a.N; i0 += kRowsThreads * 4) {
-    int l[4] = {-1, -1, -1, -1};
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-    if (i0 + 4 <= a.N) {
-      const int4 x = __ldg(reinterpret_cast<const int4*>(a.labels + i0));
-      l[0] = x.x; l[1] = x.y; l[2] = x.z; l[3] = x.w;
-      if (kBwd) {
-        const float4 y = __ldg(reinterpret_cast<const float4*>(a.dloss + i0));
-        d[0] = y.x; d[1] = y.y; d[2] = y.z; d[3] = y.w;
-      }
-    } else {
-      for (int e = 0; i0 + e < a.N; ++e) {
-        l[e] = __ldg(a.labels + i0 + e);
-        if (kBwd) d[e] = __ldg(a.dloss + i0 + e);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool live = l[e] >= 0 && l[e] < a.V;
-      total += live;
-      before += live && i0 + e < base;
-      bad |= l[e] >= a.V;
-      if (kBwd && live) big = fmaxf(big, fabsf(d[e]));
-    }
+  auto count = [&](int i, int l, float d) {
+    const bool live = l >= 0 && l < a.V;
+    total += live;
+    before += live && i < base;
+    bad |= l >= a.V;
+    if (kBwd && live) big = fmaxf(big, fabsf(d));
+  };
+  const int4* labels4 = reinterpret_cast<const int4*>(a.labels);
+  const float4* dloss4 = reinterpret_cast<const float4*>(a.dloss);
+#pragma unroll 4
+  for (int i = tid; i < a.N / 4; i += kRowsThreads) {
+    const int4 l = __ldg(labels4 + i);
+    const float4 d = kBwd ? __ldg(dloss4 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    count(4 * i, l.x, d.x);
+    count(4 * i + 1, l.y, d.y);
+    count(4 * i + 2, l.z, d.z);
+    count(4 * i + 3, l.w, d.w);
+  }
+  if (tid < (a.N & 3)) {
+    const int i = (a.N & ~3) + tid;
+    count(i, __ldg(a.labels + i), kBwd ? __ldg(a.dloss + i) : 0.f);
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) {

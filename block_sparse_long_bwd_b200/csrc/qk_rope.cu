@@ -13,11 +13,16 @@
 //   dx = r (v - n mean(v n))
 //
 // Eight lanes own a row, four pairs each (both components of a pair, so the
-// rotation needs no other lane); a warp takes four consecutive tokens of one
-// head, 512 (bf16) or 1024 (fp32) contiguous bytes.  cos, sin and gamma of a
-// lane's pairs depend on the token and not on the head, so a lane computes
-// them once, folds gamma into them and walks its heads.  The 32 - rot_dim / 2
-// "pairs" behind the rotated ones are neighbouring components at angle 0.
+// rotation needs no other lane); a warp takes four consecutive tokens and
+// walks the heads of q, then of k.  cos and sin of a lane's pairs depend on the
+// token alone, so a lane computes them once for all its heads.  The
+// 32 - rot_dim / 2 "pairs" behind the rotated ones are neighbouring components
+// at angle 0.
+//
+// The pass is bound by HBM (2 or 3 tensors cross it), and what it needs for
+// that is enough bytes in flight: each warp copies its rows a few heads ahead
+// into shared memory (cp.async, 16 bytes a lane), without registers or
+// barriers between warps.
 //
 // Angles: theta^(-2i / rot_dim) / 2 pi, a fraction of a turn per position, is
 // held as a 64-bit fixed-point number, so the product with the position
@@ -48,9 +53,9 @@ struct QkArgs {
   void* out[2];             // forward: rotated q, k; backward: dq, dk
   const float* gamma[2];    // [64] or null (ones)
   const int32_t* pos;       // [B][L] or null (the index in the sequence)
-  float* part;              // backward: [blocks][64] sums for dgamma, q's blocks then k's
+  float* part;              // backward: [2][blocks][64] sums for dgamma of q and k
   int B, H, L;
-  int hsplit;               // head ranges a tensor's heads are split into
+  int splits;               // ranges the 2 H heads of q and k are split into
   int rot, half;            // rotated components; half of it
   float eps;
   uint64_t turn[32];        // turns per position of pair i, 64-bit fixed point
@@ -77,118 +82,134 @@ struct Pairs {
   float2 a[2], b[2];
 };
 
-// A lane's part of a row as it lies in memory.
-template <typename T, int kMode>
-struct Raw;
-template <int kMode>
-struct Raw<__nv_bfloat16, kMode> {
-  uint32_t w[4];
-  static __device__ __forceinline__ float2 lohi(uint32_t x) {
-    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+// A warp's four rows in shared memory, 16-byte chunks permuted so that the
+// lanes' reads meet no bank twice: bf16 (eight chunks a row, lanes read 8 bytes)
+// swaps the row's halves in odd rows, fp32 (sixteen) its neighbours in the
+// upper half.
+template <typename T>
+struct Tile {
+  static constexpr int kRow = kHeadDim * sizeof(T), kChunks = kRow / 16;
+  static constexpr int kBytes = 4 * kRow;
+  static __device__ __forceinline__ int chunk(int row, int c) {
+    return sizeof(T) == 2 ? c ^ ((row & 1) << 2) : c ^ (c >> 3);
   }
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  // Address of component j of row `row`.
+  static __device__ __forceinline__ const T* at(const uint8_t* tile, int row, int j) {
+    const int byte = j * sizeof(T);
+    return reinterpret_cast<const T*>(tile + row * kRow + chunk(row, byte >> 4) * 16 +
+                                      (byte & 15));
+  }
+  // Copies a lane's share of its row.
+  static __device__ __forceinline__ void copy(uint8_t* tile, int row, int sub, const T* src) {
+#pragma unroll
+    for (int c = 0; c < kChunks; c += 8)
+      cp_async16(tile + row * kRow + chunk(row, c + sub) * 16,
+                 reinterpret_cast<const uint8_t*>(src) + (c + sub) * 16);
+  }
+};
+
+// A lane's four pairs of its row: from the tile, and to global memory.
+template <int kMode>
+__device__ __forceinline__ Pairs load_pairs(const QkArgs& q, const uint8_t* tile, int row, int p,
+                                            int oa, int ob, const __nv_bfloat16*) {
+  using R = Tile<__nv_bfloat16>;
+  auto lohi = [](uint32_t x) {
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+  };
+  Pairs o;
+  if (kMode == kHalves) {
+    const uint2 x = *reinterpret_cast<const uint2*>(R::at(tile, row, oa));
+    const uint2 y = *reinterpret_cast<const uint2*>(R::at(tile, row, ob));
+    o.a[0] = lohi(x.x); o.a[1] = lohi(x.y);
+    o.b[0] = lohi(y.x); o.b[1] = lohi(y.y);
+  } else if (kMode == kInterleaved) {
+    const uint4 u = *reinterpret_cast<const uint4*>(R::at(tile, row, oa));
+    const float2 x[4] = {lohi(u.x), lohi(u.y), lohi(u.z), lohi(u.w)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      o.a[i] = make_float2(x[2 * i].x, x[2 * i + 1].x);
+      o.b[i] = make_float2(x[2 * i].y, x[2 * i + 1].y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      o.a[i] = make_float2(to_f(*R::at(tile, row, comp_a<kMode>(q, p + 2 * i))),
+                           to_f(*R::at(tile, row, comp_a<kMode>(q, p + 2 * i + 1))));
+      o.b[i] = make_float2(to_f(*R::at(tile, row, comp_b<kMode>(q, p + 2 * i))),
+                           to_f(*R::at(tile, row, comp_b<kMode>(q, p + 2 * i + 1))));
+    }
+  }
+  return o;
+}
+template <int kMode>
+__device__ __forceinline__ Pairs load_pairs(const QkArgs& q, const uint8_t* tile, int row, int p,
+                                            int oa, int ob, const float*) {
+  using R = Tile<float>;
+  Pairs o;
+  if (kMode == kScattered) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      o.a[i] = make_float2(*R::at(tile, row, comp_a<kMode>(q, p + 2 * i)),
+                           *R::at(tile, row, comp_a<kMode>(q, p + 2 * i + 1)));
+      o.b[i] = make_float2(*R::at(tile, row, comp_b<kMode>(q, p + 2 * i)),
+                           *R::at(tile, row, comp_b<kMode>(q, p + 2 * i + 1)));
+    }
+    return o;
+  }
+  const float4 x = *reinterpret_cast<const float4*>(R::at(tile, row, oa));
+  const float4 y = *reinterpret_cast<const float4*>(R::at(tile, row, ob));
+  if (kMode == kInterleaved) {
+    o.a[0] = make_float2(x.x, x.z); o.a[1] = make_float2(y.x, y.z);
+    o.b[0] = make_float2(x.y, x.w); o.b[1] = make_float2(y.y, y.w);
+  } else {
+    o.a[0] = make_float2(x.x, x.y); o.a[1] = make_float2(x.z, x.w);
+    o.b[0] = make_float2(y.x, y.y); o.b[1] = make_float2(y.z, y.w);
+  }
+  return o;
+}
+template <int kMode>
+__device__ __forceinline__ void store_pairs(const QkArgs& q, __nv_bfloat16* row, int p, int oa,
+                                            int ob, const Pairs& v) {
+  auto pack = [](float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  __device__ __forceinline__ void load(const QkArgs& q, const __nv_bfloat16* row, int p, int oa,
-                                       int ob) {
-    if (kMode == kHalves) {
-      const uint2 x = *reinterpret_cast<const uint2*>(row + oa);
-      const uint2 y = *reinterpret_cast<const uint2*>(row + ob);
-      w[0] = x.x; w[1] = x.y; w[2] = y.x; w[3] = y.y;
-    } else if (kMode == kInterleaved) {
-      const uint4 x = *reinterpret_cast<const uint4*>(row + oa);
-      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    } else {
-      const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
+  };
+  if (kMode == kHalves) {
+    *reinterpret_cast<uint2*>(row + oa) =
+        make_uint2(pack(v.a[0].x, v.a[0].y), pack(v.a[1].x, v.a[1].y));
+    *reinterpret_cast<uint2*>(row + ob) =
+        make_uint2(pack(v.b[0].x, v.b[0].y), pack(v.b[1].x, v.b[1].y));
+  } else if (kMode == kInterleaved) {
+    *reinterpret_cast<uint4*>(row + oa) =
+        make_uint4(pack(v.a[0].x, v.b[0].x), pack(v.a[0].y, v.b[0].y),
+                   pack(v.a[1].x, v.b[1].x), pack(v.a[1].y, v.b[1].y));
+  } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = r[comp_a<kMode>(q, p + e)] | ((uint32_t)r[comp_b<kMode>(q, p + e)] << 16);
+    for (int e = 0; e < 4; ++e) {
+      const float x = e & 1 ? v.a[e >> 1].y : v.a[e >> 1].x;
+      const float y = e & 1 ? v.b[e >> 1].y : v.b[e >> 1].x;
+      row[comp_a<kMode>(q, p + e)] = __float2bfloat16_rn(x);
+      row[comp_b<kMode>(q, p + e)] = __float2bfloat16_rn(y);
     }
   }
-  __device__ __forceinline__ Pairs get() const {
-    Pairs o;
-    if (kMode == kHalves) {
-      o.a[0] = lohi(w[0]); o.a[1] = lohi(w[1]);
-      o.b[0] = lohi(w[2]); o.b[1] = lohi(w[3]);
-    } else {
-      const float2 x[4] = {lohi(w[0]), lohi(w[1]), lohi(w[2]), lohi(w[3])};
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        o.a[i] = make_float2(x[2 * i].x, x[2 * i + 1].x);
-        o.b[i] = make_float2(x[2 * i].y, x[2 * i + 1].y);
-      }
-    }
-    return o;
-  }
-  static __device__ __forceinline__ void store(const QkArgs& q, __nv_bfloat16* row, int p, int oa,
-                                               int ob, const Pairs& v) {
-    if (kMode == kHalves) {
-      *reinterpret_cast<uint2*>(row + oa) =
-          make_uint2(pack(v.a[0].x, v.a[0].y), pack(v.a[1].x, v.a[1].y));
-      *reinterpret_cast<uint2*>(row + ob) =
-          make_uint2(pack(v.b[0].x, v.b[0].y), pack(v.b[1].x, v.b[1].y));
-    } else if (kMode == kInterleaved) {
-      *reinterpret_cast<uint4*>(row + oa) =
-          make_uint4(pack(v.a[0].x, v.b[0].x), pack(v.a[0].y, v.b[0].y),
-                     pack(v.a[1].x, v.b[1].x), pack(v.a[1].y, v.b[1].y));
-    } else {
-      const float x[4] = {v.a[0].x, v.a[0].y, v.a[1].x, v.a[1].y};
-      const float y[4] = {v.b[0].x, v.b[0].y, v.b[1].x, v.b[1].y};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        row[comp_a<kMode>(q, p + e)] = __float2bfloat16_rn(x[e]);
-        row[comp_b<kMode>(q, p + e)] = __float2bfloat16_rn(y[e]);
-      }
-    }
-  }
-};
+}
 template <int kMode>
-struct Raw<float, kMode> {
-  float4 x, y;
-  __device__ __forceinline__ void load(const QkArgs& q, const float* row, int p, int oa, int ob) {
-    if (kMode != kScattered) {
-      x = *reinterpret_cast<const float4*>(row + oa);
-      y = *reinterpret_cast<const float4*>(row + ob);
-    } else {
-      x = make_float4(row[comp_a<kMode>(q, p)], row[comp_a<kMode>(q, p + 1)],
-                      row[comp_a<kMode>(q, p + 2)], row[comp_a<kMode>(q, p + 3)]);
-      y = make_float4(row[comp_b<kMode>(q, p)], row[comp_b<kMode>(q, p + 1)],
-                      row[comp_b<kMode>(q, p + 2)], row[comp_b<kMode>(q, p + 3)]);
-    }
-  }
-  __device__ __forceinline__ Pairs get() const {
-    Pairs o;
-    if (kMode == kInterleaved) {
-      o.a[0] = make_float2(x.x, x.z); o.a[1] = make_float2(y.x, y.z);
-      o.b[0] = make_float2(x.y, x.w); o.b[1] = make_float2(y.y, y.w);
-    } else {
-      o.a[0] = make_float2(x.x, x.y); o.a[1] = make_float2(x.z, x.w);
-      o.b[0] = make_float2(y.x, y.y); o.b[1] = make_float2(y.z, y.w);
-    }
-    return o;
-  }
-  static __device__ __forceinline__ void store(const QkArgs& q, float* row, int p, int oa, int ob,
-                                               const Pairs& v) {
-    if (kMode == kInterleaved) {
-      *reinterpret_cast<float4*>(row + oa) =
-          make_float4(v.a[0].x, v.b[0].x, v.a[0].y, v.b[0].y);
-      *reinterpret_cast<float4*>(row + ob) =
-          make_float4(v.a[1].x, v.b[1].x, v.a[1].y, v.b[1].y);
-    } else if (kMode == kHalves) {
-      *reinterpret_cast<float4*>(row + oa) = make_float4(v.a[0].x, v.a[0].y, v.a[1].x, v.a[1].y);
-      *reinterpret_cast<float4*>(row + ob) = make_float4(v.b[0].x, v.b[0].y, v.b[1].x, v.b[1].y);
-    } else {
-      const float s[4] = {v.a[0].x, v.a[0].y, v.a[1].x, v.a[1].y};
-      const float t[4] = {v.b[0].x, v.b[0].y, v.b[1].x, v.b[1].y};
+__device__ __forceinline__ void store_pairs(const QkArgs& q, float* row, int p, int oa, int ob,
+                                            const Pairs& v) {
+  if (kMode == kInterleaved) {
+    *reinterpret_cast<float4*>(row + oa) = make_float4(v.a[0].x, v.b[0].x, v.a[0].y, v.b[0].y);
+    *reinterpret_cast<float4*>(row + ob) = make_float4(v.a[1].x, v.b[1].x, v.a[1].y, v.b[1].y);
+  } else if (kMode == kHalves) {
+    *reinterpret_cast<float4*>(row + oa) = make_float4(v.a[0].x, v.a[0].y, v.a[1].x, v.a[1].y);
+    *reinterpret_cast<float4*>(row + ob) = make_float4(v.b[0].x, v.b[0].y, v.b[1].x, v.b[1].y);
+  } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        row[comp_a<kMode>(q, p + e)] = s[e];
-        row[comp_b<kMode>(q, p + e)] = t[e];
-      }
+    for (int e = 0; e < 4; ++e) {
+      row[comp_a<kMode>(q, p + e)] = e & 1 ? v.a[e >> 1].y : v.a[e >> 1].x;
+      row[comp_b<kMode>(q, p + e)] = e & 1 ? v.b[e >> 1].y : v.b[e >> 1].x;
     }
   }
-};
+}
 
 // Sum over the eight lanes of a row (a fixed tree: every lane gets the same).
 __device__ __forceinline__ float sum8(float x) {
@@ -201,44 +222,64 @@ __device__ __forceinline__ float sum8(float x) {
 __device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// A lane reads its own components of a row before it writes them and no other
-// lane touches them, so the outputs may be the inputs.
+// Heads copied ahead of the one being worked on, and the bytes of shared
+// memory a warp needs for them.
+template <typename T, bool kBwd>
+struct Ring {
+  static constexpr int kDepth = sizeof(T) == 2 ? (kBwd ? 6 : 8) : 4;
+  static constexpr int kSlot = Tile<T>::kBytes * (kBwd ? 2 : 1);
+  static constexpr int kBytes = kDepth * kSlot;
+};
+
+// A warp has read a row whole before it writes any of it, and no other warp
+// touches it, so the outputs may be the inputs.
 template <typename T, int kMode, bool kBwd>
-__global__ void __launch_bounds__(kQkThreads, kBwd ? 3 : 4)
+__global__ void __launch_bounds__(kQkThreads, 3)
     qk_rope_kernel(const __grid_constant__ QkArgs a) {
-  constexpr int kAhead = kBwd || sizeof(T) == 4 ? 2 : 4;
-  __shared__ float red[kQkThreads / 32][64];
-  const int lane = threadIdx.x & 31, p0 = (lane & 7) * 4;
-  const int t = blockIdx.y / a.hsplit;         // 0: q, 1: k
-  const int split = blockIdx.y % a.hsplit;
-  const int h0 = (int)((long long)a.H * split / a.hsplit);
-  const int h1 = (int)((long long)a.H * (split + 1) / a.hsplit);
+  using R = Ring<T, kBwd>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float red[kBwd ? 2 : 1][kQkThreads / 32][64];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = lane >> 3, sub = lane & 7, p0 = sub * 4;
+  uint8_t* ring = smem + warp * R::kBytes;
+  const int i0 = (int)(2ll * a.H * blockIdx.y / a.splits);
+  const int i1 = (int)(2ll * a.H * (blockIdx.y + 1) / a.splits);
   const long long tokens = (long long)a.B * a.L;
   const int oa = comp_a<kMode>(a, p0);
   const int ob = kMode == kInterleaved ? oa + 4 : comp_b<kMode>(a, p0);
-
-  float2 ga[2], gb[2], dga[2], dgb[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    ga[i] = gb[i] = both(1.f);
-    dga[i] = dgb[i] = both(0.f);
-    if (a.gamma[t]) {
-      const float* g = a.gamma[t];
-      ga[i] = make_float2(__ldg(g + comp_a<kMode>(a, p0 + 2 * i)),
-                          __ldg(g + comp_a<kMode>(a, p0 + 2 * i + 1)));
-      gb[i] = make_float2(__ldg(g + comp_b<kMode>(a, p0 + 2 * i)),
-                          __ldg(g + comp_b<kMode>(a, p0 + 2 * i + 1)));
-    }
+  if (kBwd) {
+    for (int i = threadIdx.x; i < 2 * (kQkThreads / 32) * 64; i += kQkThreads)
+      (&red[0][0][0])[i] = 0.f;
+    __syncthreads();
   }
 
   for (long long tb = (long long)blockIdx.x * kTokensPerBlock; tb < tokens;
        tb += (long long)gridDim.x * kTokensPerBlock) {
-    const long long token = tb + (threadIdx.x >> 3);
+    const long long token = tb + warp * 4 + row;
+    if (tb + warp * 4 >= tokens) continue;  // none of this warp's four
     // Lanes past the last token redo the last one and store nothing, so that
     // every lane reaches the shuffles.
     const bool live = token < tokens;
     const long long tok = live ? token : tokens - 1;
     const int b = (int)(tok / a.L), l = (int)(tok % a.L);
+    const size_t step = (size_t)a.L * kHeadDim;
+    const size_t base = ((size_t)b * a.H * a.L + l) * kHeadDim;  // head 0
+    // Copies item i (head i of q, or head i - H of k) into its slot.
+    auto fetch = [&](int i) {
+      if (i < i1) {
+        const int t = i >= a.H;
+        const size_t off = base + (size_t)(t ? i - a.H : i) * step;
+        uint8_t* slot = ring + (i - i0) % R::kDepth * R::kSlot;
+        Tile<T>::copy(slot, row, sub, static_cast<const T*>(a.in[t]) + off);
+        if (kBwd)
+          Tile<T>::copy(slot + Tile<T>::kBytes, row, sub, static_cast<const T*>(a.dy[t]) + off);
+      }
+      cp_async_commit();
+    };
+    __syncwarp();  // the last tile's slots are read
+#pragma unroll
+    for (int i = 0; i < R::kDepth - 1; ++i) fetch(i0 + i);
+
     const int pos = a.pos ? __ldg(a.pos + tok) : l;
     float2 c[2], s[2];
 #pragma unroll
@@ -251,37 +292,43 @@ __global__ void __launch_bounds__(kQkThreads, kBwd ? 3 : 4)
       (e & 1 ? c[e >> 1].y : c[e >> 1].x) = co;
       (e & 1 ? s[e >> 1].y : s[e >> 1].x) = si;
     }
-    // Forward: y_a = r (x_a (ga c) - x_b (gb s)), y_b = r (x_b (gb c) + x_a (ga s)).
-    float2 ca[2], sa[2], cb[2], sb[2];
-    if (!kBwd) {
+    for (int t = i0 >= a.H, i = i0; i < i1; t = 1) {
+      float2 ga[2], gb[2], dga[2], dgb[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        ca[i] = mul2(ga[i], c[i]);
-        sa[i] = mul2(ga[i], s[i]);
-        cb[i] = mul2(gb[i], c[i]);
-        sb[i] = neg2(mul2(gb[i], s[i]));
-      }
-    }
-    const size_t step = (size_t)a.L * kHeadDim;
-    size_t off = (((size_t)b * a.H + h0) * a.L + l) * kHeadDim;
-    const T* in = static_cast<const T*>(a.in[t]);
-    const T* dy = static_cast<const T*>(a.dy[t]);
-    T* out = static_cast<T*>(a.out[t]);
-    // A few heads' rows are loaded before the first is used: inputs and
-    // outputs may alias, so the compiler cannot move the loads up.
-    for (int h = h0; h < h1; h += kAhead, off += kAhead * step) {
-      Raw<T, kMode> rx[kAhead], rd[kBwd ? kAhead : 1];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (h + u < h1) {
-          rx[u].load(a, in + off + u * step, p0, oa, ob);
-          if (kBwd) rd[kBwd ? u : 0].load(a, dy + off + u * step, p0, oa, ob);
+      for (int e = 0; e < 2; ++e) {
+        ga[e] = gb[e] = both(1.f);
+        dga[e] = dgb[e] = both(0.f);
+        if (a.gamma[t]) {
+          const float* g = a.gamma[t];
+          ga[e] = make_float2(__ldg(g + comp_a<kMode>(a, p0 + 2 * e)),
+                              __ldg(g + comp_a<kMode>(a, p0 + 2 * e + 1)));
+          gb[e] = make_float2(__ldg(g + comp_b<kMode>(a, p0 + 2 * e)),
+                              __ldg(g + comp_b<kMode>(a, p0 + 2 * e + 1)));
         }
+      }
+      // Forward: y_a = r (x_a (ga c) - x_b (gb s)), y_b = r (x_b (gb c) + x_a (ga s)).
+      float2 ca[2], sa[2], cb[2], sb[2];
+      if (!kBwd) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (h + u >= h1) break;
-        const Pairs x = rx[u].get();
-        Pairs y;
+        for (int e = 0; e < 2; ++e) {
+          ca[e] = mul2(ga[e], c[e]);
+          sa[e] = mul2(ga[e], s[e]);
+          cb[e] = mul2(gb[e], c[e]);
+          sb[e] = neg2(mul2(gb[e], s[e]));
+        }
+      }
+      const int end = t ? i1 : min(i1, a.H);
+      T* out = static_cast<T*>(a.out[t]) + base + (size_t)(t ? i - a.H : i) * step;
+      for (; i < end; ++i, out += step) {
+        fetch(i + R::kDepth - 1);
+        cp_async_wait<R::kDepth - 1>();
+        __syncwarp();
+        const uint8_t* slot = ring + (i - i0) % R::kDepth * R::kSlot;
+        const Pairs x = load_pairs<kMode>(a, slot, row, p0, oa, ob, (const T*)nullptr);
+        Pairs d, y;
+        if (kBwd)
+          d = load_pairs<kMode>(a, slot + Tile<T>::kBytes, row, p0, oa, ob, (const T*)nullptr);
+        __syncwarp();  // the slot is read
         float2 sq = mul2(x.a[0], x.a[0]);
         sq = fma2(x.a[1], x.a[1], sq);
         sq = fma2(x.b[0], x.b[0], sq);
@@ -289,61 +336,66 @@ __global__ void __launch_bounds__(kQkThreads, kBwd ? 3 : 4)
         const float r = rsqrtf(fmaf(sum8(sq.x + sq.y), 1.f / kHeadDim, a.eps));
         if (!kBwd) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            y.a[i] = mul2(both(r), fma2(x.b[i], sb[i], mul2(x.a[i], ca[i])));
-            y.b[i] = mul2(both(r), fma2(x.a[i], sa[i], mul2(x.b[i], cb[i])));
+          for (int e = 0; e < 2; ++e) {
+            y.a[e] = mul2(both(r), fma2(x.b[e], sb[e], mul2(x.a[e], ca[e])));
+            y.b[e] = mul2(both(r), fma2(x.a[e], sa[e], mul2(x.b[e], cb[e])));
           }
         } else {
-          const Pairs d = rd[kBwd ? u : 0].get();
           float2 va[2], vb[2], vx = both(0.f);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int e = 0; e < 2; ++e) {
             // g = R^T dy; v = gamma g
-            const float2 g = fma2(d.b[i], s[i], mul2(d.a[i], c[i]));
-            const float2 k = fma2(d.a[i], neg2(s[i]), mul2(d.b[i], c[i]));
-            va[i] = mul2(g, ga[i]);
-            vb[i] = mul2(k, gb[i]);
-            vx = fma2(va[i], x.a[i], vx);
-            vx = fma2(vb[i], x.b[i], vx);
+            const float2 g = fma2(d.b[e], s[e], mul2(d.a[e], c[e]));
+            const float2 k = fma2(d.a[e], neg2(s[e]), mul2(d.b[e], c[e]));
+            va[e] = mul2(g, ga[e]);
+            vb[e] = mul2(k, gb[e]);
+            vx = fma2(va[e], x.a[e], vx);
+            vx = fma2(vb[e], x.b[e], vx);
             if (live) {
-              dga[i] = fma2(g, mul2(both(r), x.a[i]), dga[i]);
-              dgb[i] = fma2(k, mul2(both(r), x.b[i]), dgb[i]);
+              dga[e] = fma2(g, mul2(both(r), x.a[e]), dga[e]);
+              dgb[e] = fma2(k, mul2(both(r), x.b[e]), dgb[e]);
             }
           }
           const float m = -sum8(vx.x + vx.y) * r * r * (1.f / kHeadDim);  // -mean(v n) r
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            y.a[i] = mul2(both(r), fma2(both(m), x.a[i], va[i]));
-            y.b[i] = mul2(both(r), fma2(both(m), x.b[i], vb[i]));
+          for (int e = 0; e < 2; ++e) {
+            y.a[e] = mul2(both(r), fma2(both(m), x.a[e], va[e]));
+            y.b[e] = mul2(both(r), fma2(both(m), x.b[e], vb[e]));
           }
         }
-        if (live) Raw<T, kMode>::store(a, out + off + u * step, p0, oa, ob, y);
+        if (live) store_pairs<kMode>(a, out, p0, oa, ob, y);
+      }
+      if (kBwd) {
+        // The warp's sums of g n over its four tokens, added to those of its
+        // earlier tokens.
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = e & 1 ? dga[e >> 1].y : dga[e >> 1].x;
+          float y = e & 1 ? dgb[e >> 1].y : dgb[e >> 1].x;
+          x += __shfl_xor_sync(0xffffffffu, x, 8);
+          x += __shfl_xor_sync(0xffffffffu, x, 16);
+          y += __shfl_xor_sync(0xffffffffu, y, 8);
+          y += __shfl_xor_sync(0xffffffffu, y, 16);
+          if (lane < 8) {
+            red[t][warp][comp_a<kMode>(a, p0 + e)] += x;
+            red[t][warp][comp_b<kMode>(a, p0 + e)] += y;
+          }
+        }
       }
     }
+    cp_async_wait<0>();
   }
 
   if (kBwd) {
-    // The block's sum of g n per component, in a fixed order: over the
-    // warp's four tokens, then over its warps.
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float x = e & 1 ? dga[e >> 1].y : dga[e >> 1].x;
-      float y = e & 1 ? dgb[e >> 1].y : dgb[e >> 1].x;
-      x += __shfl_xor_sync(0xffffffffu, x, 8);
-      x += __shfl_xor_sync(0xffffffffu, x, 16);
-      y += __shfl_xor_sync(0xffffffffu, y, 8);
-      y += __shfl_xor_sync(0xffffffffu, y, 16);
-      if (lane < 8) {
-        red[threadIdx.x >> 5][comp_a<kMode>(a, p0 + e)] = x;
-        red[threadIdx.x >> 5][comp_b<kMode>(a, p0 + e)] = y;
-      }
-    }
+    // The block's sums, over its warps in order.
     __syncthreads();
-    if (threadIdx.x < 64) {
+    if (threadIdx.x < 128) {
+      const int t = threadIdx.x >> 6, j = threadIdx.x & 63;
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kQkThreads / 32; ++w) sum += red[w][threadIdx.x];
-      a.part[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 64 + threadIdx.x] = sum;
+      for (int w = 0; w < kQkThreads / 32; ++w) sum += red[t][w][j];
+      const size_t blocks = (size_t)gridDim.x * gridDim.y;
+      a.part[(t * blocks + (size_t)blockIdx.y * gridDim.x + blockIdx.x) * 64 + j] = sum;
     }
   }
 }
@@ -368,21 +420,21 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Blocks along the tokens (the backward's partial rows per head range).  A
-// block past the cap walks several token tiles.
+// Blocks along the tokens.  The backward's write a partial sum each: past the
+// cap a block walks several token tiles.
 int token_blocks(const bb_qk_desc& d, bool bwd) {
   const long long tiles = ((long long)d.B * d.L + kTokensPerBlock - 1) / kTokensPerBlock;
   const long long cap = bwd ? 1024 : 1 << 20;
   return (int)(tiles < cap ? tiles : cap);
 }
 
-// Head ranges per tensor: enough blocks to fill the GPU (four 256-thread
-// blocks on each of 148 SMs), at most one per head; longer walks share the
-// angles.
+// Ranges the 2 H heads are split into: enough blocks to fill the GPU (four
+// 256-thread blocks on each of 148 SMs), at most one per head; longer walks
+// share the angles and keep more rows in flight.
 int head_splits(const bb_qk_desc& d, bool bwd) {
-  const int want = 148 * 4, have = 2 * token_blocks(d, bwd);
+  const int want = 148 * 4, have = token_blocks(d, bwd);
   int s = (want + have - 1) / have;
-  return s < d.H ? s : d.H;
+  return s < 2 * d.H ? s : 2 * d.H;
 }
 
 int check_desc(const bb_qk_desc* d) {
@@ -402,7 +454,7 @@ QkArgs make_args(const bb_qk_desc& d, bool bwd) {
   a.B = d.B;
   a.H = d.H;
   a.L = d.L;
-  a.hsplit = head_splits(d, bwd);
+  a.splits = head_splits(d, bwd);
   a.rot = d.rot_dim;
   a.half = d.rot_dim / 2;
   a.eps = d.eps;
@@ -415,16 +467,22 @@ QkArgs make_args(const bb_qk_desc& d, bool bwd) {
   return a;
 }
 
+template <typename T, int kMode, bool kBwd>
+cudaError_t launch_as(const bb_qk_desc& d, const QkArgs& a, cudaStream_t s) {
+  constexpr int smem = kQkThreads / 32 * Ring<T, kBwd>::kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(qk_rope_kernel<T, kMode, kBwd>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  qk_rope_kernel<T, kMode, kBwd>
+      <<<dim3(token_blocks(d, kBwd), a.splits), kQkThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T, bool kBwd>
 cudaError_t launch_mode(const bb_qk_desc& d, const QkArgs& a, cudaStream_t s) {
-  const dim3 grid(token_blocks(d, kBwd), 2 * a.hsplit);
-  if (d.interleaved || a.rot == 0)
-    qk_rope_kernel<T, kInterleaved, kBwd><<<grid, kQkThreads, 0, s>>>(a);
-  else if (a.half % 4 == 0)
-    qk_rope_kernel<T, kHalves, kBwd><<<grid, kQkThreads, 0, s>>>(a);
-  else
-    qk_rope_kernel<T, kScattered, kBwd><<<grid, kQkThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  if (d.interleaved || a.rot == 0) return launch_as<T, kInterleaved, kBwd>(d, a, s);
+  if (a.half % 4 == 0) return launch_as<T, kHalves, kBwd>(d, a, s);
+  return launch_as<T, kScattered, kBwd>(d, a, s);
 }
 
 size_t part_floats(const bb_qk_desc& d) {
@@ -499,7 +557,7 @@ int bb_qk_norm_rope_bwd(const bb_qk_desc* desc, const void* q, const void* k,
                                         : launch_mode<__nv_bfloat16, true>(*desc, a, s);
   if (e != cudaSuccess) return BB_ERR_CUDA;
   if (dgamma_q || dgamma_k) {
-    qk_dgamma_kernel<<<dim3(8, 2), 256, 0, s>>>(a.part, a.hsplit * token_blocks(*desc, true),
+    qk_dgamma_kernel<<<dim3(8, 2), 256, 0, s>>>(a.part, a.splits * token_blocks(*desc, true),
                                                 dgamma_q, dgamma_k);
     if (cudaGetLastError() != cudaSuccess) return BB_ERR_CUDA;
   }

@@ -504,6 +504,21 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 16 bytes from global to shared memory without registers, in groups that are
+// waited for in order.
+__device__ __forceinline__ void cp_async16(void* smem_dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the last `kLeft` groups of this thread have arrived.
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 // 32 bytes to global memory, 32-byte aligned: one whole sector.
 __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
