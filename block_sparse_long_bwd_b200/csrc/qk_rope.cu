@@ -93,37 +93,33 @@ struct Tile {
   static __device__ __forceinline__ int chunk(int row, int c) {
     return sizeof(T) == 2 ? c ^ ((row & 1) << 2) : c ^ (c >> 3);
   }
-  // Address of component j of row `row`.
-  static __device__ __forceinline__ const T* at(const uint8_t* tile, int row, int j) {
+  // Byte offset, and address, of component j of row `row`.
+  static __device__ __forceinline__ int off(int row, int j) {
     const int byte = j * sizeof(T);
-    return reinterpret_cast<const T*>(tile + row * kRow + chunk(row, byte >> 4) * 16 +
-                                      (byte & 15));
+    return row * kRow + chunk(row, byte >> 4) * 16 + (byte & 15);
   }
-  // Copies a lane's share of its row.
-  static __device__ __forceinline__ void copy(uint8_t* tile, int row, int sub, const T* src) {
-#pragma unroll
-    for (int c = 0; c < kChunks; c += 8)
-      cp_async16(tile + row * kRow + chunk(row, c + sub) * 16,
-                 reinterpret_cast<const uint8_t*>(src) + (c + sub) * 16);
+  static __device__ __forceinline__ const T* at(const uint8_t* tile, int row, int j) {
+    return reinterpret_cast<const T*>(tile + off(row, j));
   }
 };
 
-// A lane's four pairs of its row: from the tile, and to global memory.
+// A lane's four pairs of its row: from the tile (sa, sb: where its runs lie
+// there), and to global memory (oa, ob: their first components).
 template <int kMode>
 __device__ __forceinline__ Pairs load_pairs(const QkArgs& q, const uint8_t* tile, int row, int p,
-                                            int oa, int ob, const __nv_bfloat16*) {
+                                            int sa, int sb, const __nv_bfloat16*) {
   using R = Tile<__nv_bfloat16>;
   auto lohi = [](uint32_t x) {
     return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
   };
   Pairs o;
   if (kMode == kHalves) {
-    const uint2 x = *reinterpret_cast<const uint2*>(R::at(tile, row, oa));
-    const uint2 y = *reinterpret_cast<const uint2*>(R::at(tile, row, ob));
+    const uint2 x = *reinterpret_cast<const uint2*>(tile + sa);
+    const uint2 y = *reinterpret_cast<const uint2*>(tile + sb);
     o.a[0] = lohi(x.x); o.a[1] = lohi(x.y);
     o.b[0] = lohi(y.x); o.b[1] = lohi(y.y);
   } else if (kMode == kInterleaved) {
-    const uint4 u = *reinterpret_cast<const uint4*>(R::at(tile, row, oa));
+    const uint4 u = *reinterpret_cast<const uint4*>(tile + sa);
     const float2 x[4] = {lohi(u.x), lohi(u.y), lohi(u.z), lohi(u.w)};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -143,7 +139,7 @@ __device__ __forceinline__ Pairs load_pairs(const QkArgs& q, const uint8_t* tile
 }
 template <int kMode>
 __device__ __forceinline__ Pairs load_pairs(const QkArgs& q, const uint8_t* tile, int row, int p,
-                                            int oa, int ob, const float*) {
+                                            int sa, int sb, const float*) {
   using R = Tile<float>;
   Pairs o;
   if (kMode == kScattered) {
@@ -156,8 +152,8 @@ __device__ __forceinline__ Pairs load_pairs(const QkArgs& q, const uint8_t* tile
     }
     return o;
   }
-  const float4 x = *reinterpret_cast<const float4*>(R::at(tile, row, oa));
-  const float4 y = *reinterpret_cast<const float4*>(R::at(tile, row, ob));
+  const float4 x = *reinterpret_cast<const float4*>(tile + sa);
+  const float4 y = *reinterpret_cast<const float4*>(tile + sb);
   if (kMode == kInterleaved) {
     o.a[0] = make_float2(x.x, x.z); o.a[1] = make_float2(y.x, y.z);
     o.b[0] = make_float2(x.y, x.w); o.b[1] = make_float2(y.y, y.w);
@@ -247,6 +243,11 @@ __global__ void __launch_bounds__(kQkThreads, 3)
   const long long tokens = (long long)a.B * a.L;
   const int oa = comp_a<kMode>(a, p0);
   const int ob = kMode == kInterleaved ? oa + 4 : comp_b<kMode>(a, p0);
+  // Where the lane's copies and runs lie in a tile.
+  constexpr int kRun = 16 / sizeof(T);  // components of a 16-byte chunk
+  const int cp0 = Tile<T>::off(row, sub * kRun);
+  const int cp1 = sizeof(T) == 4 ? Tile<T>::off(row, (sub + 8) * kRun) : 0;
+  const int sh_a = Tile<T>::off(row, oa), sh_b = Tile<T>::off(row, ob);
   if (kBwd) {
     for (int i = threadIdx.x; i < 2 * (kQkThreads / 32) * 64; i += kQkThreads)
       (&red[0][0][0])[i] = 0.f;
@@ -264,21 +265,34 @@ __global__ void __launch_bounds__(kQkThreads, 3)
     const int b = (int)(tok / a.L), l = (int)(tok % a.L);
     const size_t step = (size_t)a.L * kHeadDim;
     const size_t base = ((size_t)b * a.H * a.L + l) * kHeadDim;  // head 0
-    // Copies item i (head i of q, or head i - H of k) into its slot.
-    auto fetch = [&](int i) {
-      if (i < i1) {
-        const int t = i >= a.H;
-        const size_t off = base + (size_t)(t ? i - a.H : i) * step;
-        uint8_t* slot = ring + (i - i0) % R::kDepth * R::kSlot;
-        Tile<T>::copy(slot, row, sub, static_cast<const T*>(a.in[t]) + off);
-        if (kBwd)
-          Tile<T>::copy(slot + Tile<T>::kBytes, row, sub, static_cast<const T*>(a.dy[t]) + off);
+    // Copies the next item (a head of q, after q's last one of k) into the
+    // next slot.
+    int fi = i0, fs = 0;
+    const size_t first = base + (size_t)(i0 < a.H ? i0 : i0 - a.H) * step + sub * kRun;
+    const T* fx = static_cast<const T*>(a.in[i0 >= a.H]) + first;
+    const T* fd = static_cast<const T*>(a.dy[i0 >= a.H]) + first;
+    auto fetch = [&]() {
+      if (fi < i1) {
+        uint8_t* slot = ring + fs;
+        cp_async16(slot + cp0, fx);
+        if (sizeof(T) == 4) cp_async16(slot + cp1, fx + 8 * kRun);
+        if (kBwd) {
+          cp_async16(slot + Tile<T>::kBytes + cp0, fd);
+          if (sizeof(T) == 4) cp_async16(slot + Tile<T>::kBytes + cp1, fd + 8 * kRun);
+          fd += step;
+        }
+        fx += step;
+        fs = fs == R::kBytes - R::kSlot ? 0 : fs + R::kSlot;
+        if (++fi == a.H) {
+          fx = static_cast<const T*>(a.in[1]) + base + sub * kRun;
+          if (kBwd) fd = static_cast<const T*>(a.dy[1]) + base + sub * kRun;
+        }
       }
       cp_async_commit();
     };
     __syncwarp();  // the last tile's slots are read
 #pragma unroll
-    for (int i = 0; i < R::kDepth - 1; ++i) fetch(i0 + i);
+    for (int i = 0; i < R::kDepth - 1; ++i) fetch();
 
     const int pos = a.pos ? __ldg(a.pos + tok) : l;
     float2 c[2], s[2];
@@ -292,6 +306,7 @@ __global__ void __launch_bounds__(kQkThreads, 3)
       (e & 1 ? c[e >> 1].y : c[e >> 1].x) = co;
       (e & 1 ? s[e >> 1].y : s[e >> 1].x) = si;
     }
+    int rs = 0;  // slot of the item being worked on
     for (int t = i0 >= a.H, i = i0; i < i1; t = 1) {
       float2 ga[2], gb[2], dga[2], dgb[2];
 #pragma unroll
@@ -320,14 +335,16 @@ __global__ void __launch_bounds__(kQkThreads, 3)
       const int end = t ? i1 : min(i1, a.H);
       T* out = static_cast<T*>(a.out[t]) + base + (size_t)(t ? i - a.H : i) * step;
       for (; i < end; ++i, out += step) {
-        fetch(i + R::kDepth - 1);
+        fetch();
         cp_async_wait<R::kDepth - 1>();
         __syncwarp();
-        const uint8_t* slot = ring + (i - i0) % R::kDepth * R::kSlot;
-        const Pairs x = load_pairs<kMode>(a, slot, row, p0, oa, ob, (const T*)nullptr);
+        const uint8_t* slot = ring + rs;
+        rs = rs == R::kBytes - R::kSlot ? 0 : rs + R::kSlot;
+        const Pairs x = load_pairs<kMode>(a, slot, row, p0, sh_a, sh_b, (const T*)nullptr);
         Pairs d, y;
         if (kBwd)
-          d = load_pairs<kMode>(a, slot + Tile<T>::kBytes, row, p0, oa, ob, (const T*)nullptr);
+          d = load_pairs<kMode>(a, slot + Tile<T>::kBytes, row, p0, sh_a, sh_b,
+                                (const T*)nullptr);
         __syncwarp();  // the slot is read
         float2 sq = mul2(x.a[0], x.a[0]);
         sq = fma2(x.a[1], x.a[1], sq);
