@@ -13,8 +13,7 @@ import os
 
 import torch
 
-_HERE = os.path.dirname(os.path.abspath(__file__))
-LIB_PATH = os.path.join(_HERE, "libbbattn.so")
+LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbbattn.so")
 
 BB_OK = 0
 BB_ERR_WORKSPACE = -4
@@ -381,14 +380,16 @@ def _dtype_code(t, name):
 def _dense(t, name, dtype, device, shape=None):
     """Checks of one argument: contiguous, on CUDA device number `device`, of
     the dtype and (where given) shape."""
+    if (t.get_device() == device >= 0 and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on cuda:{device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}")
 
 
 def _like(t, name, ref):
@@ -407,9 +408,12 @@ def _scope(device, stream):
         if stream.device.index != device:
             raise ValueError(f"stream must be on cuda:{device}")
         return torch.cuda.stream(stream)
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():
         return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    return _HERE
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _current_stream_ptr(device):
@@ -502,10 +506,9 @@ def bb_qk_norm_rope_bwd(desc, q, k, gamma_q, gamma_k, positions, dq_out, dk_out,
                          gamma_q, gamma_k, positions)
     with _scope(device, stream):
         dq, dk = _like(dq, "dq", q), _like(dk, "dk", k)
-        dgamma = torch.empty((2, desc.d), dtype=torch.float32, device=q.device)
+        dgamma = q.new_empty((2, desc.d), dtype=torch.float32)
         if workspace is None:
-            workspace = torch.empty(bb_qk_norm_rope_workspace_size(desc), dtype=torch.uint8,
-                                    device=q.device)
+            workspace = q.new_empty(bb_qk_norm_rope_workspace_size(desc), dtype=torch.uint8)
         _dense(workspace, "workspace", workspace.dtype, device)
         _check(lib().bb_qk_norm_rope_bwd(
             ctypes.byref(desc), q.data_ptr(), k.data_ptr(), _ptr(gamma_q), _ptr(gamma_k),
@@ -513,7 +516,7 @@ def bb_qk_norm_rope_bwd(desc, q, k, gamma_q, gamma_k, positions, dq_out, dk_out,
             dgamma.data_ptr(), dgamma.data_ptr() + 4 * desc.d, workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), _current_stream_ptr(device)),
             "bb_qk_norm_rope_bwd")
-    return dq, dk, dgamma[0], dgamma[1]
+    return dq, dk, *dgamma.unbind(0)
 
 
 def bb_linear_ce_workspace_size(N, hidden, V, pass_):
@@ -542,15 +545,14 @@ def _ce_tensors(h, w, bias, labels):
 def _fp32(t, name, n, h):
     """t, or a new tensor where it is None: fp32 [n] on h's device."""
     if t is None:
-        return torch.empty(n, dtype=torch.float32, device=h.device)
+        return h.new_empty(n, dtype=torch.float32)
     _dense(t, name, torch.float32, h.get_device(), (n,))
     return t
 
 
 def _ce_workspace(workspace, N, hidden, V, pass_, h):
     if workspace is None:
-        return torch.empty(bb_linear_ce_workspace_size(N, hidden, V, pass_), dtype=torch.uint8,
-                           device=h.device)
+        return h.new_empty(bb_linear_ce_workspace_size(N, hidden, V, pass_), dtype=torch.uint8)
     _dense(workspace, "workspace", workspace.dtype, h.get_device())
     return workspace
 

@@ -173,6 +173,28 @@ bool tc_bwd_plan_fused(const Problem& p);
 cudaError_t launch_plan_bwd(const Problem& p, cudaStream_t s);
 cudaError_t launch_simt_bwd(const Problem& p, cudaStream_t s, EventMarks* marks);
 
+// A launch whose kernel waits for the one in front on the device (grid_wait),
+// so that its setup runs under that one's end; pair: in clusters of two.
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, int threads, size_t smem,
+                           bool pair, cudaStream_t s, Args... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = pair ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- device helpers -----------------------------------------------------
 
 __device__ __forceinline__ float to_f(float x) { return x; }

@@ -1050,28 +1050,6 @@ char* body(void* workspace) {
   return reinterpret_cast<char*>(((uintptr_t)workspace + 511) & ~(uintptr_t)255);
 }
 
-// Launches that wait for the one in front on the device (grid_wait), so that
-// their setup runs under its end.
-template <typename... Params, typename... Args>
-cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, int threads, size_t smem,
-                           bool pair, cudaStream_t s, Args... args) {
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = pair ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int kMode, bool kPair>
 cudaError_t launch_gemm_as(const CeArgs& a, long long tiles, int sms, const CUtensorMap& h,
                            const CUtensorMap& hp, const CUtensorMap& w, const CUtensorMap& dz,

@@ -254,6 +254,8 @@ __global__ void __launch_bounds__(kQkThreads, 3)
     __syncthreads();
   }
 
+  grid_launch_dependents();
+
   for (long long tb = (long long)blockIdx.x * kTokensPerBlock; tb < tokens;
        tb += (long long)gridDim.x * kTokensPerBlock) {
     const long long token = tb + warp * 4 + row;
@@ -417,23 +419,26 @@ __global__ void __launch_bounds__(kQkThreads, 3)
   }
 }
 
-// dgamma of q (block.y 0) and k (1): the blocks' partial sums, in order.
-// Eight components per block, 32 partial rows at a time.
+// dgamma of q (blocks 0-7) and k: the blocks' partial sums, in order.  Eight
+// components per block, 32 partial rows at a time.
 __global__ void __launch_bounds__(256)
     qk_dgamma_kernel(const float* part, int rows, float* dgq, float* dgk) {
   __shared__ float red[32][8];
   const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
-  const float* p = part + (size_t)blockIdx.y * rows * 64 + blockIdx.x * 8 + c;
+  const int t = blockIdx.x >> 3, j = (blockIdx.x & 7) * 8 + c;
+  const float* p = part + (size_t)t * rows * 64 + j;
   float s = 0.f;
+  grid_wait();
+#pragma unroll 4
   for (int i = g; i < rows; i += 32) s += p[(size_t)i * 64];
   red[g][c] = s;
   __syncthreads();
   if (g == 0) {
-    float t = 0.f;
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) t += red[i][c];
-    float* out = blockIdx.y ? dgk : dgq;
-    if (out) out[blockIdx.x * 8 + c] = t;
+    for (int i = 0; i < 32; ++i) sum += red[i][c];
+    float* out = t ? dgk : dgq;
+    if (out) out[j] = sum;
   }
 }
 
@@ -574,9 +579,9 @@ int bb_qk_norm_rope_bwd(const bb_qk_desc* desc, const void* q, const void* k,
                                         : launch_mode<__nv_bfloat16, true>(*desc, a, s);
   if (e != cudaSuccess) return BB_ERR_CUDA;
   if (dgamma_q || dgamma_k) {
-    qk_dgamma_kernel<<<dim3(8, 2), 256, 0, s>>>(a.part, a.splits * token_blocks(*desc, true),
-                                                dgamma_q, dgamma_k);
-    if (cudaGetLastError() != cudaSuccess) return BB_ERR_CUDA;
+    if (launch_chained(qk_dgamma_kernel, 16, 256, 0, false, s, (const float*)a.part,
+                       a.splits * token_blocks(*desc, true), dgamma_q, dgamma_k) != cudaSuccess)
+      return BB_ERR_CUDA;
   }
   return BB_OK;
 }
