@@ -40,7 +40,8 @@ def _labels(N, V, share, g):
 @pytest.mark.parametrize("N,D,V,share", [
     (1, 64, 1, 1.0), (1, 64, 300, 1.0), (3, 72, 257, 0.6), (128, 128, 256, 1.0),
     (129, 136, 1000, 1.0), (200, 256, 511, 0.4), (700, 320, 1537, 0.9), (64, 768, 5003, 1.0),
-    (300, 776, 20011, 0.3), (2500, 64, 4096, 1.0), (257, 1024, 9001, 0.0)])
+    (300, 776, 20011, 0.3), (2500, 64, 4096, 1.0), (257, 1024, 9001, 0.0),
+    (100, 200, 3001, 0.0), (1, 64, 40, 0.0), (128, 512, 30011, 0.5), (65, 1544, 700, 1.0)])
 def test_exact_integer_gradients(N, D, V, share):
     g = torch.Generator().manual_seed(N + V)
     half = D // 2
