@@ -314,10 +314,11 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-// Arrive on a barrier of the cluster by its mapped address; orders this
-// thread's tensor-memory reads (after tcgen05.fence::before_thread_sync).
+// Arrive on a barrier of the cluster by its mapped address.  Relaxed, as
+// mbar_arrive is: it hands over tensor memory, ordered by the tcgen05 fences;
+// a release would wait for the thread's global stores in flight.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
                : "memory");
 }
 // 2-D tiled load into this CTA's shared memory that signals a barrier of the
