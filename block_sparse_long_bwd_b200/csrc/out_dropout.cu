@@ -15,6 +15,7 @@
 // ~100 integer operations a call needs (6 per element) fit beside that.
 #include "common.cuh"
 #include "dropout.cuh"
+#include "sm100.cuh"
 
 namespace bb {
 namespace {
@@ -31,47 +32,82 @@ struct DropArgs {
   uint32_t site, k0, k1;
 };
 
-__device__ __forceinline__ void load16(const float* p, float (&v)[kGroup]) {
+// The 16 elements of a group as 32-bit words: by whole 32-byte sectors where
+// the tensors are aligned to them (kWide), else by 16 bytes.
+template <bool kWide, int kWords>
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[kWords]) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const float4 f = reinterpret_cast<const float4*>(p)[c];
-    v[4 * c] = f.x; v[4 * c + 1] = f.y; v[4 * c + 2] = f.z; v[4 * c + 3] = f.w;
+  for (int c = 0; c < kWords; c += 8) {
+    uint32_t u[8];
+    if (kWide) {
+      sm100::ld_global_32(static_cast<const uint32_t*>(p) + c, u);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 x = reinterpret_cast<const uint4*>(p)[c / 4 + h];
+        u[4 * h] = x.x; u[4 * h + 1] = x.y; u[4 * h + 2] = x.z; u[4 * h + 3] = x.w;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[c + e] = u[e];
   }
 }
 
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[kGroup]) {
+template <bool kWide, int kWords>
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[kWords]) {
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const uint4 u = reinterpret_cast<const uint4*>(p)[c];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  for (int c = 0; c < kWords; c += 8) {
+    if (kWide) {
+      const uint32_t u[8] = {w[c], w[c + 1], w[c + 2], w[c + 3],
+                             w[c + 4], w[c + 5], w[c + 6], w[c + 7]};
+      sm100::st_global_32(static_cast<uint32_t*>(p) + c, u);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[8 * c + 2 * j] = __uint_as_float(w[j] << 16);
-      v[8 * c + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      for (int h = 0; h < 8; h += 4)
+        reinterpret_cast<uint4*>(p)[(c + h) / 4] =
+            make_uint4(w[c + h], w[c + h + 1], w[c + h + 2], w[c + h + 3]);
     }
   }
 }
 
-__device__ __forceinline__ void store16(float* p, const float (&v)[kGroup]) {
+template <bool kWide>
+__device__ __forceinline__ void load16(const float* p, float (&v)[kGroup]) {
+  uint32_t w[16];
+  load_words<kWide>(p, w);
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    reinterpret_cast<float4*>(p)[c] =
-        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  for (int e = 0; e < kGroup; ++e) v[e] = __uint_as_float(w[e]);
 }
 
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[kGroup]) {
+template <bool kWide>
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[kGroup]) {
+  uint32_t w[8];
+  load_words<kWide>(p, w);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    __nv_bfloat162 h[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[8 * c + 2 * j], v[8 * c + 2 * j + 1]);
-    reinterpret_cast<uint4*>(p)[c] = *reinterpret_cast<const uint4*>(h);
+  for (int e = 0; e < 8; ++e) {
+    v[2 * e] = __uint_as_float(w[e] << 16);
+    v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
   }
+}
+
+template <bool kWide>
+__device__ __forceinline__ void store16(float* p, const float (&v)[kGroup]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int e = 0; e < kGroup; ++e) w[e] = __float_as_uint(v[e]);
+  store_words<kWide>(p, w);
+}
+
+template <bool kWide>
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[kGroup]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = sm100::pack_bf16(v[2 * e], v[2 * e + 1]);
+  store_words<kWide>(p, w);
 }
 
 // x and out, or residual and out, may be the same buffer: a thread reads its
 // elements before it writes them and no other thread touches them.
-template <typename T, bool kResidual>
+template <typename T, bool kResidual, bool kWide>
 __global__ void __launch_bounds__(256) out_dropout_kernel(const DropArgs a) {
   const uint64_t g = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const uint64_t i0 = g * kGroup;
@@ -81,8 +117,8 @@ __global__ void __launch_bounds__(256) out_dropout_kernel(const DropArgs a) {
   T* out = static_cast<T*>(a.out) + i0;
   if (i0 + kGroup <= a.n) {
     float v[kGroup], w[kGroup];
-    load16(x, v);
-    if (kResidual) load16(r, w);
+    load16<kWide>(x, v);
+    if (kResidual) load16<kWide>(r, w);
     const uint32_t keep =
         keep16(philox4x32_10(make_uint4((uint32_t)g, (uint32_t)(g >> 32), a.site, 0xFFFFFFFFu),
                              a.k0, a.k1),
@@ -96,7 +132,7 @@ __global__ void __launch_bounds__(256) out_dropout_kernel(const DropArgs a) {
       else
         v[e] = k ? v[e] * a.scale : 0.f;
     }
-    store16(out, v);
+    store16<kWide>(out, v);
   } else {
     // The last, partial group.
     const uint32_t keep =
@@ -112,14 +148,16 @@ __global__ void __launch_bounds__(256) out_dropout_kernel(const DropArgs a) {
   }
 }
 
-template <typename T>
+// 32-byte accesses: fp32 without residual, 9.25 M elements, 12.3 us against
+// 16.4 by 16 bytes; bf16 with residual, 16.8 M elements, 16.4 either way.
+template <typename T, bool kWide>
 cudaError_t launch(const DropArgs& a, cudaStream_t s) {
   const uint64_t groups = (a.n + kGroup - 1) / kGroup;
   const unsigned grid = (unsigned)((groups + 255) / 256);
   if (a.residual)
-    out_dropout_kernel<T, true><<<grid, 256, 0, s>>>(a);
+    out_dropout_kernel<T, true, kWide><<<grid, 256, 0, s>>>(a);
   else
-    out_dropout_kernel<T, false><<<grid, 256, 0, s>>>(a);
+    out_dropout_kernel<T, false, kWide><<<grid, 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -135,8 +173,12 @@ int run_dropout(uint64_t n, int dtype, float rate, uint64_t seed, uint32_t site,
   if (n > (1ull << 42)) return BB_ERR_UNSUPPORTED;
   DropArgs a{x, residual, out, n, thr * 0x01010101u, scale, site, (uint32_t)seed,
              (uint32_t)(seed >> 32)};
-  const cudaError_t e = dtype == BB_F32 ? launch<float>(a, (cudaStream_t)stream)
-                                        : launch<__nv_bfloat16>(a, (cudaStream_t)stream);
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool wide = (((uintptr_t)x | (uintptr_t)residual | (uintptr_t)out) & 31u) == 0;
+  const cudaError_t e =
+      dtype == BB_F32
+          ? (wide ? launch<float, true>(a, st) : launch<float, false>(a, st))
+          : (wide ? launch<__nv_bfloat16, true>(a, st) : launch<__nv_bfloat16, false>(a, st));
   return e == cudaSuccess ? BB_OK : BB_ERR_CUDA;
 }
 

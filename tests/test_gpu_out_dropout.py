@@ -46,6 +46,23 @@ def test_forward_and_backward(n, dtype, residual):
     _check(bb.bb_dropout_bwd(d, 0.1, SEED, 3), d, None, 0.1, SEED, 3)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_tensors_aligned_to_16_bytes_only(dtype):
+    """Every mixture of 16- and 32-byte alignment gives the same bits."""
+    n, off = 5003, 16 // torch.finfo(dtype).bits * 8
+    g = torch.Generator().manual_seed(4)
+    base = [torch.randn(n, generator=g).to(dtype).cuda() for _ in range(2)]
+    want = bb.bb_dropout_fwd(base[0], base[1], 0.1, 8)
+    for which in range(8):
+        t = []
+        for k in range(3):
+            buf = torch.empty(n + off, dtype=dtype, device="cuda")
+            t.append(buf[off:] if which >> k & 1 else buf[:n])
+        t[0].copy_(base[0])
+        t[1].copy_(base[1])
+        assert torch.equal(bb.bb_dropout_fwd(t[0], t[1], 0.1, 8, out=t[2]), want), which
+
+
 @pytest.mark.parametrize("rate", [0.0, 0.001, 0.5, 255 / 256])
 def test_rates(rate):
     x = torch.randn(3, 5, 771, device="cuda")
