@@ -176,7 +176,7 @@ cudaError_t launch_simt_bwd(const Problem& p, cudaStream_t s, EventMarks* marks)
 // A launch whose kernel waits for the one in front on the device (grid_wait),
 // so that its setup runs under that one's end; pair: in clusters of two.
 template <typename... Params, typename... Args>
-cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, int threads, size_t smem,
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
                            bool pair, cudaStream_t s, Args... args) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -186,7 +186,7 @@ cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, int threads
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

@@ -770,6 +770,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int base = blockIdx.x * a.per_block;
   grid_launch_dependents();
+  grid_wait();
   int total = 0, before = 0, bad = 0;
   float big = 0.f;
   auto count = [&](int i, int l, float d) {
@@ -894,6 +895,7 @@ __global__ void __launch_bounds__(256)
                      const int* idx, float* loss, float* lse) {
   __shared__ float2 sh[8][33];
   const int r = threadIdx.x & 7, g = threadIdx.x >> 3;
+  grid_launch_dependents();
   grid_wait();
   const int rows = info->rows;
   if ((int)blockIdx.x * 8 >= rows) return;
@@ -943,6 +945,7 @@ __global__ void __launch_bounds__(256)
   const size_t n = i / chunks;
   const bool live = n < (size_t)N;
   const int c = (int)(i % chunks) * 8;
+  grid_launch_dependents();
   grid_wait();
   const int p = live ? pos[n] : -1;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -1135,8 +1138,9 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
   r.idx = reinterpret_cast<int*>(ws + p.idx);
   r.lab = reinterpret_cast<int*>(ws + p.lab);
   r.hp = reinterpret_cast<uint16_t*>(ws + p.hp);
-  rows_kernel<false><<<(N + r.per_block - 1) / r.per_block, kRowsThreads, 0, s>>>(r);
-  if (cudaGetLastError() != cudaSuccess) return BB_ERR_CUDA;
+  if (launch_chained(rows_kernel<false>, (N + r.per_block - 1) / r.per_block, kRowsThreads, 0,
+                     false, s, r) != cudaSuccess)
+    return BB_ERR_CUDA;
   CeArgs a{};
   a.N = N;
   a.D = hidden;
@@ -1203,8 +1207,9 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   r.rlse = reinterpret_cast<float*>(ws + p.rlse);
   r.dls = reinterpret_cast<float*>(ws + p.dls);
   r.hp = reinterpret_cast<uint16_t*>(ws + p.hp);
-  rows_kernel<true><<<(N + r.per_block - 1) / r.per_block, kRowsThreads, 0, s>>>(r);
-  if (cudaGetLastError() != cudaSuccess) return BB_ERR_CUDA;
+  if (launch_chained(rows_kernel<true>, (N + r.per_block - 1) / r.per_block, kRowsThreads, 0,
+                     false, s, r) != cudaSuccess)
+    return BB_ERR_CUDA;
   CeArgs a{};
   a.N = N;
   a.D = hidden;

@@ -109,6 +109,8 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[kGrou
 // elements before it writes them and no other thread touches them.
 template <typename T, bool kResidual, bool kWide>
 __global__ void __launch_bounds__(256) out_dropout_kernel(const DropArgs a) {
+  sm100::grid_launch_dependents();
+  sm100::grid_wait();
   const uint64_t g = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const uint64_t i0 = g * kGroup;
   if (i0 >= a.n) return;
@@ -154,11 +156,9 @@ template <typename T, bool kWide>
 cudaError_t launch(const DropArgs& a, cudaStream_t s) {
   const uint64_t groups = (a.n + kGroup - 1) / kGroup;
   const unsigned grid = (unsigned)((groups + 255) / 256);
-  if (a.residual)
-    out_dropout_kernel<T, true, kWide><<<grid, 256, 0, s>>>(a);
-  else
-    out_dropout_kernel<T, false, kWide><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_chained(a.residual ? out_dropout_kernel<T, true, kWide>
+                                   : out_dropout_kernel<T, false, kWide>,
+                        grid, 256, 0, false, s, a);
 }
 
 int run_dropout(uint64_t n, int dtype, float rate, uint64_t seed, uint32_t site, const void* x,

@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(kQkThreads, 3)
   }
 
   grid_launch_dependents();
+  grid_wait();
 
   for (long long tb = (long long)blockIdx.x * kTokensPerBlock; tb < tokens;
        tb += (long long)gridDim.x * kTokensPerBlock) {
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(256)
   const int t = blockIdx.x >> 3, j = (blockIdx.x & 7) * 8 + c;
   const float* p = part + (size_t)t * rows * 64 + j;
   float s = 0.f;
+  grid_launch_dependents();
   grid_wait();
 #pragma unroll 4
   for (int i = g; i < rows; i += 32) s += p[(size_t)i * 64];
@@ -495,9 +497,8 @@ cudaError_t launch_as(const bb_qk_desc& d, const QkArgs& a, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(qk_rope_kernel<T, kMode, kBwd>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  qk_rope_kernel<T, kMode, kBwd>
-      <<<dim3(token_blocks(d, kBwd), a.splits), kQkThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_chained(qk_rope_kernel<T, kMode, kBwd>, dim3(token_blocks(d, kBwd), a.splits),
+                        kQkThreads, smem, false, s, a);
 }
 
 template <typename T, bool kBwd>
