@@ -743,7 +743,6 @@ struct RowsArgs {
   uint16_t* hp;         // packed rows of h
 };
 
-constexpr int kRowsPerBlock = 32;  // at most; a lane of warp 0 each
 constexpr int kRowsThreads = 256;
 
 __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
@@ -756,8 +755,7 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
   return s;
 }
 
-// Block b takes per_block rows (8 of up to 1024 rows, one per warp; 32 of
-// more, so that fewer blocks read the labels): it packs those that have a label and
+// Block b takes per_block rows, 32 at a time: it packs those that have a label and
 // computes their label's logit in fp32.  Each block reads all labels (and
 // dloss) to find how many rows with a label lie before its own, so one
 // launch does; labels are a few KB to a few hundred and come from L2.
@@ -765,8 +763,7 @@ template <bool kBwd>
 __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
   __shared__ int cnt[3][8];
   __shared__ float mx[8];
-  static_assert(kRowsPerBlock == 32, "one lane of a warp per row");
-  __shared__ int dst[kRowsPerBlock], lab[kRowsPerBlock];
+  __shared__ int dst[32], lab[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int base = blockIdx.x * a.per_block;
   grid_launch_dependents();
@@ -818,65 +815,69 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
     big = fmaxf(big, mx[w]);
   }
   const float dlref = big > 0.f && big < INFINITY ? big : 1.f;
-  if (warp == 0) {
-    const int n = lane < a.per_block ? base + lane : a.N;
-    const int l = n < a.N ? __ldg(a.labels + n) : -1;
-    const bool live = l >= 0 && l < a.V;
-    const unsigned m = __ballot_sync(0xffffffffu, live);
-    const int p = before + __popc(m & ((1u << lane) - 1));
-    dst[lane] = live ? p : -1;
-    lab[lane] = l;
-    if (live) {
-      a.idx[p] = n;
-      a.lab[p] = l;
-      if (kBwd) {
-        a.rlse[p] = __ldg(a.lse + n);
-        a.dls[p] = __ldg(a.dloss + n) / dlref;
-      }
-    }
-    if (n < a.N) {
-      if (kBwd) {
-        a.pos[n] = live ? p : -1;
-      } else if (!live) {
-        a.loss[n] = 0.f;
-        a.lse_out[n] = 0.f;
-      }
-    }
-    if (blockIdx.x == 0 && lane == 0) {
-      a.info->status = bad ? BB_ERR_BAD_LABEL : BB_OK;
-      a.info->rows = total;
-      a.info->direct = total == a.N;
-      a.info->dlref = dlref;
-    }
+  if (blockIdx.x == 0 && tid == 0) {
+    a.info->status = bad ? BB_ERR_BAD_LABEL : BB_OK;
+    a.info->rows = total;
+    a.info->direct = total == a.N;
+    a.info->dlref = dlref;
   }
-  __syncthreads();
   const int chunks = a.D / 8;  // 16-byte pieces of a row
   const bool pack = total != a.N;
-  for (int r = warp; r < a.per_block; r += 8) {
-    const int p = dst[r];
-    if (p < 0) continue;
-    const uint4* src = reinterpret_cast<const uint4*>(a.h + (size_t)(base + r) * a.D);
-    const uint4* wl = reinterpret_cast<const uint4*>(a.w + (size_t)lab[r] * a.D);
-    uint4* out = reinterpret_cast<uint4*>(a.hp + (size_t)p * a.D);
-    float s = 0.f;
-    for (int c0 = 0; c0 < chunks; c0 += 128) {
-      uint4 x[4], y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c0 + 32 * i + lane < chunks) {
-          x[i] = __ldg(src + c0 + 32 * i + lane);
-          y[i] = __ldg(wl + c0 + 32 * i + lane);
+  for (int r0 = 0; r0 < a.per_block; r0 += 32) {
+    if (warp == 0) {
+      const int n = r0 + lane < a.per_block ? base + r0 + lane : a.N;
+      const int l = n < a.N ? __ldg(a.labels + n) : -1;
+      const bool live = l >= 0 && l < a.V;
+      const unsigned m = __ballot_sync(0xffffffffu, live);
+      const int p = before + __popc(m & ((1u << lane) - 1));
+      before += __popc(m);
+      dst[lane] = live ? p : -1;
+      lab[lane] = l;
+      if (live) {
+        a.idx[p] = n;
+        a.lab[p] = l;
+        if (kBwd) {
+          a.rlse[p] = __ldg(a.lse + n);
+          a.dls[p] = __ldg(a.dloss + n) / dlref;
         }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c0 + 32 * i + lane < chunks) {
-          s = dot8(x[i], y[i], s);
-          if (pack) out[c0 + 32 * i + lane] = x[i];
+      }
+      if (n < a.N) {
+        if (kBwd) {
+          a.pos[n] = live ? p : -1;
+        } else if (!live) {
+          a.loss[n] = 0.f;
+          a.lse_out[n] = 0.f;
         }
+      }
     }
+    __syncthreads();
+    for (int r = warp; r < 32; r += 8) {
+      const int p = dst[r];
+      if (p < 0) continue;
+      const uint4* src = reinterpret_cast<const uint4*>(a.h + (size_t)(base + r0 + r) * a.D);
+      const uint4* wl = reinterpret_cast<const uint4*>(a.w + (size_t)lab[r] * a.D);
+      uint4* out = reinterpret_cast<uint4*>(a.hp + (size_t)p * a.D);
+      float s = 0.f;
+      for (int c0 = 0; c0 < chunks; c0 += 128) {
+        uint4 x[4], y[4];
 #pragma unroll
-    for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-    if (lane == 0) a.zl[p] = s + (a.bias ? __ldg(a.bias + lab[r]) : 0.f);
+        for (int i = 0; i < 4; ++i)
+          if (c0 + 32 * i + lane < chunks) {
+            x[i] = __ldg(src + c0 + 32 * i + lane);
+            y[i] = __ldg(wl + c0 + 32 * i + lane);
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c0 + 32 * i + lane < chunks) {
+            s = dot8(x[i], y[i], s);
+            if (pack) out[c0 + 32 * i + lane] = x[i];
+          }
+      }
+#pragma unroll
+      for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+      if (lane == 0) a.zl[p] = s + (a.bias ? __ldg(a.bias + lab[r]) : 0.f);
+    }
+    __syncthreads();
   }
   // The rest of the last 64 packed rows, which dW's last K step reads, is
   // zero (times the zeros of dz).
@@ -991,9 +992,8 @@ size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int make_plan(int N, int D, int V, int pass, Plan* p) {
   if (N <= 0 || D <= 0 || V <= 0 || (pass != 0 && pass != 1)) return BB_ERR_INVALID;
-  if (D % 8 != 0 || D < 64 || D > 65536 || N > (1 << 24) || V > (1 << 24))
+  if (D % 8 != 0 || D < 64 || D > 65536 || N > (1 << 20) || V > (1 << 24))
     return BB_ERR_UNSUPPORTED;
-  if ((long long)N * V >= (1ll << 44)) return BB_ERR_UNSUPPORTED;  // tile counts
   p->pair = N > kBM;
   const int tm = p->pair ? 2 * kBM : kBM;
   p->Np = (int)up(N, tm);
@@ -1082,6 +1082,10 @@ cudaError_t launch_gemm(const Plan& p, const CeArgs& a, int sms, const CUtensorM
                 : launch_gemm_as<kMode, false>(a, tiles, sms, h, hp, w, dz, dw, dh, s);
 }
 
+// Up to 1024 rows one for each of a block's warps; above, as many more as
+// keep the blocks, which each read all labels, at 512.
+int rows_per_block(int N) { return N <= 1024 ? 8 : 32 * ((N + 16383) / 16384); }
+
 int sm_count() {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -1124,7 +1128,7 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
     return BB_ERR_CUDA;
   RowsArgs r{};
   r.N = N;
-  r.per_block = N <= 1024 ? 8 : kRowsPerBlock;
+  r.per_block = rows_per_block(N);
   r.D = hidden;
   r.V = V;
   r.labels = labels;
@@ -1190,7 +1194,7 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
     return BB_ERR_CUDA;
   RowsArgs r{};
   r.N = N;
-  r.per_block = N <= 1024 ? 8 : kRowsPerBlock;
+  r.per_block = rows_per_block(N);
   r.D = hidden;
   r.V = V;
   r.labels = labels;

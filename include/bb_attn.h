@@ -364,8 +364,8 @@ BB_API int bb_qk_norm_rope_bwd(const bb_qk_desc* desc, const void* q, const void
  *   loss, lse [N] fp32, device (written)
  *   workspace device, >= bb_linear_ce_workspace_size(N, hidden, V, 0) bytes,
  *             16-byte aligned; its status word is read by bb_attn_check_status
- * Requires hidden % 8 == 0, 64 <= hidden <= 65536 and N, V <= 2^24, else
- * BB_ERR_UNSUPPORTED; N, V >= 1. */
+ * Requires hidden % 8 == 0, 64 <= hidden <= 65536, N <= 2^20 and V <= 2^24,
+ * else BB_ERR_UNSUPPORTED; N, V >= 1. */
 BB_API int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w,
                             const float* bias, const int32_t* labels, float* loss, float* lse,
                             void* workspace, size_t workspace_bytes, void* stream);
@@ -378,7 +378,9 @@ BB_API int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void*
  * The logits are computed again, a piece of the vocabulary at a time: the
  * workspace holds dz of one piece (at most 256 MiB, 512 columns at least),
  * never of all.  dz is rounded to bf16 for the two products (dbias is summed
- * before that rounding); sums are fp32 and dh, dw are rounded once.
+ * before that rounding); sums are fp32 and dh, dw are rounded once.  dz is
+ * held relative to the largest |dloss|: rows whose dloss is below 2^-100 of it
+ * lose precision.
  *   lse      [N] fp32, device, as bb_linear_ce_fwd wrote it
  *   dh       [N][hidden] bf16, device (written)
  *   dw       [V][hidden] bf16, device (written)

@@ -41,7 +41,8 @@ def _labels(N, V, share, g):
     (1, 64, 1, 1.0), (1, 64, 300, 1.0), (3, 72, 257, 0.6), (128, 128, 256, 1.0),
     (129, 136, 1000, 1.0), (200, 256, 511, 0.4), (700, 320, 1537, 0.9), (64, 768, 5003, 1.0),
     (300, 776, 20011, 0.3), (2500, 64, 4096, 1.0), (257, 1024, 9001, 0.0),
-    (100, 200, 3001, 0.0), (1, 64, 40, 0.0), (128, 512, 30011, 0.5), (65, 1544, 700, 1.0)])
+    (100, 200, 3001, 0.0), (1, 64, 40, 0.0), (128, 512, 30011, 0.5), (65, 1544, 700, 1.0),
+    (40003, 64, 300, 0.7)])
 def test_exact_integer_gradients(N, D, V, share):
     g = torch.Generator().manual_seed(N + V)
     half = D // 2
@@ -254,3 +255,46 @@ def test_streams_and_graphs():
         el, es = bb.bb_linear_ce_fwd(h, w, b, new)
         eg = bb.bb_linear_ce_bwd(h, w, b, new, es, dl)
         assert torch.equal(gl, el) and all(torch.equal(x, y) for x, y in zip(gg, eg))
+
+
+def _guarded(shape, dtype):
+    """A tensor between two guards of 4 KB, and a check that they are intact."""
+    n = int(np.prod(shape))
+    item = torch.empty(0, dtype=dtype).element_size()
+    raw = torch.full((8192 + n * item,), 0x5A, dtype=torch.uint8, device="cuda")
+    ok = lambda: bool((raw[:4096] == 0x5A).all() and (raw[4096 + n * item:] == 0x5A).all())
+    return raw[4096:4096 + n * item].view(dtype).view(shape), ok
+
+
+@pytest.mark.parametrize("N,D,V,share", [(5, 72, 131, 0.6), (128, 328, 1001, 1.0),
+                                         (301, 136, 777, 0.5), (512, 64, 256, 1.0)])
+def test_nothing_is_written_outside_the_buffers(N, D, V, share):
+    h, w, b, labels, dl = (t.cuda() for t in _general(N, D, V, share, True, N))
+    shapes = dict(loss=((N,), torch.float32), lse=((N,), torch.float32), dh=((N, D), torch.bfloat16),
+                  dw=((V, D), torch.bfloat16), dbias=((V,), torch.float32),
+                  wf=((bb.bb_linear_ce_workspace_size(N, D, V, 0),), torch.uint8),
+                  wb=((bb.bb_linear_ce_workspace_size(N, D, V, 1),), torch.uint8))
+    t = {n: _guarded(*v) for n, v in shapes.items()}
+    keep = [x.clone() for x in (h, w, b, labels, dl)]
+    bb.bb_linear_ce_fwd(h, w, b, labels, loss=t["loss"][0], lse=t["lse"][0], workspace=t["wf"][0])
+    bb.bb_linear_ce_bwd(h, w, b, labels, t["lse"][0], dl, dh=t["dh"][0], dw=t["dw"][0],
+                        dbias=t["dbias"][0], workspace=t["wb"][0])
+    torch.cuda.synchronize()
+    assert all(ok() for _, ok in t.values())
+    assert all(torch.equal(x, y) for x, y in zip(keep, (h, w, b, labels, dl)))
+    loss, lse = bb.bb_linear_ce_fwd(h, w, b, labels)
+    assert torch.equal(loss, t["loss"][0]) and torch.equal(lse, t["lse"][0])
+
+
+def test_workspace_aligned_to_16_bytes_only():
+    h, w, b, labels, dl = (t.cuda() for t in _general(90, 128, 1000, 0.8, True, 5))
+    loss, lse = bb.bb_linear_ce_fwd(h, w, b, labels)
+    want = bb.bb_linear_ce_bwd(h, w, b, labels, lse, dl)
+    for off in (16, 240, 272):
+        ws = [torch.full((bb.bb_linear_ce_workspace_size(90, 128, 1000, p) + off,), 0xFF,
+                         dtype=torch.uint8, device="cuda")[off:] for p in (0, 1)]
+        got = bb.bb_linear_ce_fwd(h, w, b, labels, workspace=ws[0])
+        assert torch.equal(got[0], loss) and torch.equal(got[1], lse)
+        got = bb.bb_linear_ce_bwd(h, w, b, labels, lse, dl, workspace=ws[1])
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert bb.bb_attn_check_status(ws[1]) == 0
