@@ -23,10 +23,11 @@
 // that is enough bytes in flight: each warp copies its rows a few heads ahead
 // into shared memory (cp.async, 16 bytes a lane), without registers or
 // barriers between warps.  Loading a few heads into registers instead took
-// 28.0 and 85.6 us where this takes 24.6 and 64.4 (forward of 4 x 16 x 4096
-// rows of q and k, gradients of 8 x 12 x 4096, bf16): 5.4 and 4.7 TB/s.  The
-// gradients then keep the issue slots 70 % busy (unpacking, the rotation, two
-// sums over the row), which bounds them before HBM does.
+// 28.0 and 85.6 us where this takes 24.9 and 59.4 (forward of 4 x 16 x 4096
+// rows of q and k, gradients of 8 x 12 x 4096, bf16): 5.4 and 5.1 TB/s.  The
+// issue slots are then about 70 % busy (unpacking, the rotation, two sums over
+// the row), which bounds the gradients before HBM does; two heads at a time
+// took them from 65.8 us (and the fp32 ones of 12 x 5003 from 21.2 to 22.1).
 //
 // Angles: theta^(-2i / rot_dim) / 2 pi, a fraction of a turn per position, is
 // held as a 64-bit fixed-point number, so the product with the position
@@ -92,7 +93,7 @@ struct Pairs {
 // upper half.
 template <typename T>
 struct Tile {
-  static constexpr int kRow = kHeadDim * sizeof(T), kChunks = kRow / 16;
+  static constexpr int kRow = kHeadDim * sizeof(T);
   static constexpr int kBytes = 4 * kRow;
   static __device__ __forceinline__ int chunk(int row, int c) {
     return sizeof(T) == 2 ? c ^ ((row & 1) << 2) : c ^ (c >> 3);
@@ -222,19 +223,20 @@ __device__ __forceinline__ float sum8(float x) {
 __device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// Heads copied ahead of the one being worked on, and the bytes of shared
-// memory a warp needs for them.
+// A warp works on two heads at a time (their waits and bookkeeping are
+// shared): slots of two heads, and the bytes of shared memory a warp needs.
 template <typename T, bool kBwd>
 struct Ring {
-  static constexpr int kDepth = sizeof(T) == 2 ? (kBwd ? 6 : 8) : 4;
-  static constexpr int kSlot = Tile<T>::kBytes * (kBwd ? 2 : 1);
+  static constexpr int kDepth = sizeof(T) == 2 ? (kBwd ? 3 : 4) : 2;
+  static constexpr int kItem = Tile<T>::kBytes * (kBwd ? 2 : 1);
+  static constexpr int kSlot = 2 * kItem;
   static constexpr int kBytes = kDepth * kSlot;
 };
 
 // A warp has read a row whole before it writes any of it, and no other warp
 // touches it, so the outputs may be the inputs.
 template <typename T, int kMode, bool kBwd>
-__global__ void __launch_bounds__(kQkThreads, 3)
+__global__ void __launch_bounds__(kQkThreads, kBwd ? 2 : 3)
     qk_rope_kernel(const __grid_constant__ QkArgs a) {
   using R = Ring<T, kBwd>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -272,25 +274,33 @@ __global__ void __launch_bounds__(kQkThreads, 3)
     const int b = (int)(tok / a.L), l = (int)(tok % a.L);
     const size_t step = (size_t)a.L * kHeadDim;
     const size_t base = ((size_t)b * a.H * a.L + l) * kHeadDim;  // head 0
-    // Copies the next item (a head of q, after q's last one of k) into the
+    // Copies the next two items (heads of q, after q's last one of k) into the
     // next slot.
-    int fi = i0, fs = 0;
+    int fi = i0, fe = i0 < a.H ? min(i1, a.H) : i1, fs = 0;
     const size_t first = base + (size_t)(i0 < a.H ? i0 : i0 - a.H) * step + sub * kRun;
     const T* fx = static_cast<const T*>(a.in[i0 >= a.H]) + first;
     const T* fd = static_cast<const T*>(a.dy[i0 >= a.H]) + first;
     auto fetch = [&]() {
       if (fi < i1) {
         uint8_t* slot = ring + fs;
-        cp_async16(slot + cp0, fx);
-        if (sizeof(T) == 4) cp_async16(slot + cp1, fx + 8 * kRun);
-        if (kBwd) {
-          cp_async16(slot + Tile<T>::kBytes + cp0, fd);
-          if (sizeof(T) == 4) cp_async16(slot + Tile<T>::kBytes + cp1, fd + 8 * kRun);
-          fd += step;
-        }
-        fx += step;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (u == 0 || fi + 1 < fe) {
+            cp_async16(slot + u * R::kItem + cp0, fx + u * step);
+            if (sizeof(T) == 4) cp_async16(slot + u * R::kItem + cp1, fx + u * step + 8 * kRun);
+            if (kBwd) {
+              uint8_t* dst = slot + u * R::kItem + Tile<T>::kBytes;
+              cp_async16(dst + cp0, fd + u * step);
+              if (sizeof(T) == 4) cp_async16(dst + cp1, fd + u * step + 8 * kRun);
+            }
+          }
         fs = fs == R::kBytes - R::kSlot ? 0 : fs + R::kSlot;
-        if (++fi == a.H) {
+        fi += 2;
+        fx += 2 * step;
+        if (kBwd) fd += 2 * step;
+        if (fi >= fe && fe < i1) {  // on to k
+          fi = a.H;
+          fe = i1;
           fx = static_cast<const T*>(a.in[1]) + base + sub * kRun;
           if (kBwd) fd = static_cast<const T*>(a.dy[1]) + base + sub * kRun;
         }
@@ -341,53 +351,76 @@ __global__ void __launch_bounds__(kQkThreads, 3)
       }
       const int end = t ? i1 : min(i1, a.H);
       T* out = static_cast<T*>(a.out[t]) + base + (size_t)(t ? i - a.H : i) * step;
-      for (; i < end; ++i, out += step) {
+      for (; i < end; i += 2, out += 2 * step) {
         fetch();
         cp_async_wait<R::kDepth - 1>();
         __syncwarp();
         const uint8_t* slot = ring + rs;
         rs = rs == R::kBytes - R::kSlot ? 0 : rs + R::kSlot;
-        const Pairs x = load_pairs<kMode>(a, slot, row, p0, sh_a, sh_b, (const T*)nullptr);
-        Pairs d, y;
-        if (kBwd)
-          d = load_pairs<kMode>(a, slot + Tile<T>::kBytes, row, p0, sh_a, sh_b,
-                                (const T*)nullptr);
+        const bool two = i + 1 < end;  // (else the second one's work is discarded)
+        Pairs x[2], d[2];
+        float ss[2], vs[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t* it = slot + (u && two ? R::kItem : 0);
+          x[u] = load_pairs<kMode>(a, it, row, p0, sh_a, sh_b, (const T*)nullptr);
+          if (kBwd)
+            d[u] = load_pairs<kMode>(a, it + Tile<T>::kBytes, row, p0, sh_a, sh_b,
+                                     (const T*)nullptr);
+        }
         __syncwarp();  // the slot is read
-        float2 sq = mul2(x.a[0], x.a[0]);
-        sq = fma2(x.a[1], x.a[1], sq);
-        sq = fma2(x.b[0], x.b[0], sq);
-        sq = fma2(x.b[1], x.b[1], sq);
-        const float r = rsqrtf(fmaf(sum8(sq.x + sq.y), 1.f / kHeadDim, a.eps));
-        if (!kBwd) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            y.a[e] = mul2(both(r), fma2(x.b[e], sb[e], mul2(x.a[e], ca[e])));
-            y.b[e] = mul2(both(r), fma2(x.a[e], sa[e], mul2(x.b[e], cb[e])));
-          }
-        } else {
-          float2 va[2], vb[2], vx = both(0.f);
+        for (int u = 0; u < 2; ++u) {
+          float2 sq = mul2(x[u].a[0], x[u].a[0]);
+          sq = fma2(x[u].a[1], x[u].a[1], sq);
+          sq = fma2(x[u].b[0], x[u].b[0], sq);
+          sq = fma2(x[u].b[1], x[u].b[1], sq);
+          ss[u] = sq.x + sq.y;
+          if (kBwd) {
+            // d becomes g = R^T dy; v = gamma g
+            float2 vx = both(0.f);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // g = R^T dy; v = gamma g
-            const float2 g = fma2(d.b[e], s[e], mul2(d.a[e], c[e]));
-            const float2 k = fma2(d.a[e], neg2(s[e]), mul2(d.b[e], c[e]));
-            va[e] = mul2(g, ga[e]);
-            vb[e] = mul2(k, gb[e]);
-            vx = fma2(va[e], x.a[e], vx);
-            vx = fma2(vb[e], x.b[e], vx);
-            if (live) {
-              dga[e] = fma2(g, mul2(both(r), x.a[e]), dga[e]);
-              dgb[e] = fma2(k, mul2(both(r), x.b[e]), dgb[e]);
+            for (int e = 0; e < 2; ++e) {
+              const float2 g = fma2(d[u].b[e], s[e], mul2(d[u].a[e], c[e]));
+              const float2 k = fma2(d[u].a[e], neg2(s[e]), mul2(d[u].b[e], c[e]));
+              vx = fma2(mul2(g, ga[e]), x[u].a[e], vx);
+              vx = fma2(mul2(k, gb[e]), x[u].b[e], vx);
+              d[u].a[e] = g;
+              d[u].b[e] = k;
             }
-          }
-          const float m = -sum8(vx.x + vx.y) * r * r * (1.f / kHeadDim);  // -mean(v n) r
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            y.a[e] = mul2(both(r), fma2(both(m), x.a[e], va[e]));
-            y.b[e] = mul2(both(r), fma2(both(m), x.b[e], vb[e]));
+            vs[u] = vx.x + vx.y;
           }
         }
-        if (live) store_pairs<kMode>(a, out, p0, oa, ob, y);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          ss[u] = sum8(ss[u]);
+          if (kBwd) vs[u] = sum8(vs[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (u && !two) break;
+          const float r = rsqrtf(fmaf(ss[u], 1.f / kHeadDim, a.eps));
+          Pairs y;
+          if (!kBwd) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              y.a[e] = mul2(both(r), fma2(x[u].b[e], sb[e], mul2(x[u].a[e], ca[e])));
+              y.b[e] = mul2(both(r), fma2(x[u].a[e], sa[e], mul2(x[u].b[e], cb[e])));
+            }
+          } else {
+            const float m = -vs[u] * r * r * (1.f / kHeadDim);  // -mean(v n) r
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (live) {
+                dga[e] = fma2(d[u].a[e], mul2(both(r), x[u].a[e]), dga[e]);
+                dgb[e] = fma2(d[u].b[e], mul2(both(r), x[u].b[e]), dgb[e]);
+              }
+              y.a[e] = mul2(both(r), fma2(both(m), x[u].a[e], mul2(d[u].a[e], ga[e])));
+              y.b[e] = mul2(both(r), fma2(both(m), x[u].b[e], mul2(d[u].b[e], gb[e])));
+            }
+          }
+          if (live) store_pairs<kMode>(a, out + u * step, p0, oa, ob, y);
+        }
       }
       if (kBwd) {
         // The warp's sums of g n over its four tokens, added to those of its
