@@ -6,7 +6,7 @@
 #include <algorithm>
 #include <vector>
 
-#include "common.cuh"
+#include "layer.cuh"
 
 namespace bb {
 

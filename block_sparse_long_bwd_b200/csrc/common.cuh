@@ -17,20 +17,6 @@ constexpr int kMaxBlocks = 8192;   // nb limit (CSR builder keeps counts in smem
 constexpr int kMaxRand = 32;       // r limit (attended list fits in smem)
 constexpr float kLog2e = 1.4426950408889634f;
 
-inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-// Dropout rate in [0, 1), rounded to 1/256: the byte threshold and 1 / keep
-// probability.  False for a rate outside [0, 1) or one that rounds to 1
-// (it would drop everything: infinite scale).
-inline bool resolve_dropout(float rate, uint32_t* thr, float* scale) {
-  if (!(rate >= 0.f && rate < 1.f)) return false;
-  const int t = (int)((double)rate * 256.0 + 0.5);
-  if (t > 255) return false;
-  *thr = (uint32_t)t;
-  *scale = (float)(256.0 / (256.0 - t));
-  return true;
-}
-
 // Everything a kernel needs about one call, passed by value.
 struct Problem {
   int B, H, L, d, bs, r, nb, dtype;
@@ -132,9 +118,6 @@ bool encode_tensor_maps(const Problem& p, int pass, TensorMaps* tm);
 // box box_inner x box_rows, 128-byte swizzle (box_inner = 64).
 bool encode_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
                     uint64_t row_stride, uint32_t box_inner, uint32_t box_rows);
-// The same for fp32 (row stride a multiple of 4, box_inner = 32).
-bool encode_f32_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
-                   uint64_t row_stride, uint32_t box_inner, uint32_t box_rows);
 
 // Tensor-core path (bf16, block 64, d 64).
 bool tc_fwd_supported(const Problem& p);
@@ -172,28 +155,6 @@ cudaError_t launch_csr_build(const Problem& p, cudaStream_t s);
 bool tc_bwd_plan_fused(const Problem& p);
 cudaError_t launch_plan_bwd(const Problem& p, cudaStream_t s);
 cudaError_t launch_simt_bwd(const Problem& p, cudaStream_t s, EventMarks* marks);
-
-// A launch whose kernel waits for the one in front on the device (grid_wait),
-// so that its setup runs under that one's end; pair: in clusters of two.
-template <typename... Params, typename... Args>
-cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
-                           bool pair, cudaStream_t s, Args... args) {
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = pair ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 // ---- device helpers -----------------------------------------------------
 

@@ -35,8 +35,7 @@
 // dloss enters it relative to the largest |dloss| and that factor is applied
 // in fp32 at the end, so for equal dloss a dz near -1 (a label of low
 // probability) is exact and no rounding is shared by all rows.
-#include "common.cuh"
-#include "sm100.cuh"
+#include "layer.cuh"
 
 namespace bb {
 namespace {

@@ -15,9 +15,8 @@
 // ~100 integer operations a call needs (6 per element) fit beside that.
 // Measured back to back: bf16 with residual, 16.8 M elements, 16.5 us (6.1
 // TB/s, 94 % of a copy's rate); fp32 gradient, 9.25 M, 12.7 us (5.8 TB/s).
-#include "common.cuh"
+#include "layer.cuh"
 #include "dropout.cuh"
-#include "sm100.cuh"
 
 namespace bb {
 namespace {

@@ -22,8 +22,7 @@
 // swizzle) and write them with TMA stores.  Output tiles are ordered M-major
 // (the 256-column tiles of one 128-row block run together), so an A block is
 // read from HBM once and from L2 for the other column tiles.
-#include "common.cuh"
-#include "sm100.cuh"
+#include "layer.cuh"
 
 namespace bb {
 namespace {

@@ -35,8 +35,7 @@
 // 2^-24 half turns (the float conversion) at every 32-bit position.
 #include <math.h>
 
-#include "common.cuh"
-#include "sm100.cuh"
+#include "layer.cuh"
 
 namespace bb {
 namespace {

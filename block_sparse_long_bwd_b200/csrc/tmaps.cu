@@ -2,7 +2,7 @@
 // fetched with cudaGetDriverEntryPoint so the library does not link libcuda.
 #include <mutex>
 
-#include "common.cuh"
+#include "layer.cuh"
 
 namespace bb {
 namespace {
