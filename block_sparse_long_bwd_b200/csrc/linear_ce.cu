@@ -8,20 +8,21 @@
 //
 // Rows whose label is outside [0, V) have no loss: their loss and dh are 0
 // and they are neither multiplied nor read into any result.  The first
-// launch (rows_kernel) packs the rows that have one, in order; when every
-// row has one, h is used where it lies.
+// launch (rows_kernel) packs the rows that have one, in order, and sums their
+// labels' logits in fp32; when every row has one, h is used where it lies.
 //
 // Forward: one GEMM over (row tile, vocabulary tile); the epilogue keeps, per
-// row of a tile, the maximum and the sum of exponentials of its 256 logits
-// and the label's logit, and a small launch merges the tiles' pairs in a
-// fixed order.  Logits live in tensor memory and registers only.
+// row, the maximum and the sum of exponentials of its columns of the tile, and
+// a small launch merges these pairs in a fixed order.  Logits live in tensor
+// memory and registers only.
 //
 // Backward: the vocabulary goes by in pieces whose dz (bf16) fits a fixed
 // workspace.  Per piece, one GEMM launch computes the logits again and
 // writes dz, and one GEMM launch forms the piece's rows of dW (complete) and
-// its part of dh, added to an fp32 sum.  A last launch rounds dh and sums
-// dbias.  Without the stored logits this is 6 R D V operations (R rows with
-// a label) beside the forward's 2 R D V.
+// its part of dh, added to an fp32 sum (one addition per element and launch,
+// so the order is fixed); dbias comes from column sums of dz taken before its
+// rounding.  A last launch rounds dh.  Without the stored logits this is
+// 6 R D V operations (R rows with a label) beside the forward's 2 R D V.
 //
 // What bounds it, measured on a B200.  Many rows: the tensor cores, and over
 // longer runs the power limit (clocks settle near 1.3 GHz): the forward of
@@ -31,7 +32,9 @@
 // the launches' own latencies: 13 rows of 768 x 30011 20 us (46 MB; 7 at a
 // copy's rate), the gradients of 77 rows 55 (94 MB; 14.5).
 //
-// dz is held in bf16, the type of the tensor-core operands it multiplies;
+// dz lies in panels of 64 columns, [Vp / 64][Np][64], so that every box that is
+// stored or loaded is one piece of memory.  It is held in bf16, the type of the
+// tensor-core operands it multiplies;
 // dloss enters it relative to the largest |dloss| and that factor is applied
 // in fp32 at the end, so for equal dloss a dz near -1 (a label of low
 // probability) is exact and no rounding is shared by all rows.
@@ -56,8 +59,8 @@ enum Mode { kLse = 0, kDz = 1, kGrad = 2 };
 // single CTAs take 128 x 128 logits (enough tiles to keep every SM loading)
 // and 128 x 256 gradients.  There a dW tile's B, up to 128 rows of 256 columns
 // of h, is the same for every tile of those columns: it stays in shared
-// memory while the CTA walks down the words, and the freed stages hold A's.  Two accumulators, so that a tile's epilogue runs
-// under the next one's MMAs.
+// memory while the CTA walks down the words, and the freed stages hold A's.
+// Two accumulators, so that a tile's epilogue runs under the next one's MMAs.
 template <int kMode, bool kPair>
 struct Cfg {
   static constexpr int kCtas = kPair ? 2 : 1;
@@ -65,10 +68,10 @@ struct Cfg {
   static constexpr int kTN = kPair || kMode == kGrad ? 256 : 128;
   static constexpr int kEpi = 8;                           // epilogue warps
   static constexpr int kCols = kTN / (kEpi / 4);           // columns of one (logits)
-  static constexpr int kSlots = kMode == kGrad ? 2 : 0;    // staging blocks of one
+  static constexpr int kSlots = kMode == kLse ? 0 : kMode == kDz ? 1 : 2;  // staging blocks of one
   static constexpr uint32_t kBTile = kTN / kCtas * kBK * 2;
   static constexpr uint32_t kStage = kATile + kBTile;
-  static constexpr int kStages = kPair ? 5 : kMode == kGrad ? 3 : 6;
+  static constexpr int kStages = kMode == kLse && !kPair ? 6 : kPair || kMode == kDz ? 5 : 3;
   static constexpr uint32_t kOut = kEpi * kSlots * 4096;   // 32 x 128 B staging blocks
   static constexpr uint32_t kSmem = 1024 + kStages * kStage + kOut;
   static constexpr int kThreads = 64 + 32 * kEpi;
@@ -102,8 +105,7 @@ struct CeArgs {
   const float* rlse;   //   lse,
   const float* dls;    //   dloss / dlref,
   const float* zl;     //   logit of the label (rows_kernel)
-  uint16_t* dz;        // [Vp / 64][Np][64]: panels of 64 columns
-  float2* part;        // [column runs of an epilogue warp][Np] (max, sum of exponentials)
+  float2* part;        // [Plan::runs][Np] (max, sum of exponentials)
   float* dbp;          // [Np / 128][Vp] column sums of dz, or null
   float* dbias;        // [V], with dbp
 };
@@ -612,13 +614,27 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
               for (int e = 0; e < 16; ++e) z[e] = make_float2(0.f, 0.f);
             }
             __syncwarp();
-            uint16_t* out = a.dz + ((size_t)((j.n0 + cbeg + c) / 64) * a.Np + row) * 64 + (c & 32);
+            // Staged and stored by TMA: 32-byte stores of a row per lane took the
+            // gradients of 1024 rows 4 % longer, those of 8192 1.6 %.
+            if ((c & 32) == 0) {
+              // The previous block's store has read the staging block.
+              if (lane == 0) bulk_wait_read_all();
+              __syncwarp();
+            }
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              uint32_t u[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) u[e] = pack_bf16(z[8 * ch + e].x, z[8 * ch + e].y);
-              st_global_32(out + 16 * ch, u);
+            for (int ch = 0; ch < 4; ++ch)
+              *reinterpret_cast<uint4*>(rowp + ((((c & 32) / 8 + ch) ^ swz) << 4)) =
+                  make_uint4(pack_bf16(z[4 * ch].x, z[4 * ch].y),
+                             pack_bf16(z[4 * ch + 1].x, z[4 * ch + 1].y),
+                             pack_bf16(z[4 * ch + 2].x, z[4 * ch + 2].y),
+                             pack_bf16(z[4 * ch + 3].x, z[4 * ch + 3].y));
+            if (c & 32) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&tmDz, stage, 0, (j.n0 + cbeg + c) / 64 * a.Np + j.m0 + r0);
+                bulk_commit_group();
+              }
             }
             if (a.dbp) red[acc][quarter][cbeg + c + lane] = column_sums(z, lane);
           }
@@ -717,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
       }
       release(acc);
     }
-    if (kMode == kGrad && lane == 0) bulk_wait_all();  // output stores complete
+    if (kMode != kLse && lane == 0) bulk_wait_all();  // output stores complete
   }
 
   // Neither CTA leaves while the other may still signal its barriers.
@@ -1188,14 +1204,15 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   if (!workspace || workspace_bytes < p.total) return BB_ERR_WORKSPACE;
   char* ws = body(workspace);
   cudaStream_t s = (cudaStream_t)stream;
-  CUtensorMap tmH, tmHp, tmW, tmH64, tmHp64, tmW64, tmDz, tmDw, tmDh;
+  CUtensorMap tmH, tmHp, tmW, tmH64, tmHp64, tmW64, tmDz32, tmDz64, tmDw, tmDh;
   if (!encode_bf16_2d(&tmH, h, hidden, N, hidden, 64, p.a_rows) ||
       !encode_bf16_2d(&tmHp, ws + p.hp, hidden, p.Np, hidden, 64, p.a_rows) ||
       !encode_bf16_2d(&tmW, w, hidden, V, hidden, 64, 128) ||
       !encode_bf16_2d(&tmH64, h, hidden, N, hidden, 64, 64) ||
       !encode_bf16_2d(&tmHp64, ws + p.hp, hidden, p.Np, hidden, 64, 64) ||
       !encode_bf16_2d(&tmW64, w, hidden, V, hidden, 64, 64) ||
-      !encode_bf16_2d(&tmDz, ws + p.dz, 64, (uint64_t)p.Vp / 64 * p.Np, 64, 64, 64) ||
+      !encode_bf16_2d(&tmDz32, ws + p.dz, 64, (uint64_t)p.Vp / 64 * p.Np, 64, 64, 32) ||
+      !encode_bf16_2d(&tmDz64, ws + p.dz, 64, (uint64_t)p.Vp / 64 * p.Np, 64, 64, 64) ||
       !encode_bf16_2d(&tmDw, dw, hidden, V, hidden, 64, 32) ||
       !encode_f32_2d(&tmDh, ws + p.dh, hidden, (uint64_t)p.splits * p.Np, hidden, 32, 32))
     return BB_ERR_CUDA;
@@ -1235,7 +1252,6 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   a.rlse = r.rlse;
   a.dls = r.dls;
   a.zl = r.zl;
-  a.dz = reinterpret_cast<uint16_t*>(ws + p.dz);
   a.dbp = dbias ? reinterpret_cast<float*>(ws + p.dbp) : nullptr;
   a.dbias = dbias;
   const int sms = sm_count();
@@ -1243,8 +1259,8 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
     a.v0 = i * p.Vp;
     a.vn = V - a.v0 < p.Vp ? V - a.v0 : p.Vp;
     a.add = i > 0;
-    if (launch_gemm<kDz>(p, a, sms, tmH, tmHp, tmW, tmW, tmW, tmW, s) != cudaSuccess ||
-        launch_gemm<kGrad>(p, a, sms, tmH64, tmHp64, tmW64, tmDz, tmDw, tmDh, s) != cudaSuccess)
+    if (launch_gemm<kDz>(p, a, sms, tmH, tmHp, tmW, tmDz32, tmW, tmW, s) != cudaSuccess ||
+        launch_gemm<kGrad>(p, a, sms, tmH64, tmHp64, tmW64, tmDz64, tmDw, tmDh, s) != cudaSuccess)
       return BB_ERR_CUDA;
   }
   const size_t pieces = (size_t)N * (hidden / 8);
