@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(kQkThreads, kBwd ? 2 : 3)
           if (live) store_pairs<kMode>(a, out + u * step, p0, oa, ob, y);
         }
       }
+      i = end;  // (an odd range of q leaves i one past it, on k's second head)
       if (kBwd) {
         // The warp's sums of g n over its four tokens, added to those of its
         // earlier tokens.

@@ -79,6 +79,24 @@ def test_forward_and_backward(B, H, L, rot, inter, dtype):
             _check_bwd(out[i], out[2 + i], t[i], gam[i], pn, t[2 + i], args)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,H,L,rot,inter", [
+    (2, 5, 2111, 16, True), (1, 1, 19001, 64, False), (1, 3, 9500, 62, False),
+    (1, 4, 6400, 64, True), (3, 7, 1100, 64, False)])
+def test_a_block_walks_heads_of_both(B, H, L, rot, inter, dtype):
+    """Enough tokens that a block's range of heads runs over several of them,
+    odd numbers of q's and on into k's.  (dgamma: 2^-16 as above; 594 token
+    blocks are 19 adds in each of 32 partial sums.)"""
+    t, gam, _ = _inputs(B, H, L, dtype, L)
+    desc = bb.make_qk_desc(B, H, L, dtype, rot_dim=rot, interleaved=inter)
+    args = (float(np.float32(1e-6)), 10000.0, rot, inter)
+    y = bb.bb_qk_norm_rope_fwd(desc, t[0], t[1], *gam)
+    out = bb.bb_qk_norm_rope_bwd(desc, t[0], t[1], *gam, None, t[2], t[3])
+    for i in range(2):
+        _check_fwd(y[i], t[i], gam[i], None, args)
+        _check_bwd(out[i], out[2 + i], t[i], gam[i], None, t[2 + i], args)
+
+
 def test_far_positions_and_other_options():
     """The angle is reduced exactly: the largest positions are as good as
     the first (the oracle's fp64 angle is within 2^31 2^-53 of exact)."""
