@@ -68,10 +68,13 @@ struct Cfg {
   static constexpr int kTN = kPair || kMode == kGrad ? 256 : 128;
   static constexpr int kEpi = 8;                           // epilogue warps
   static constexpr int kCols = kTN / (kEpi / 4);           // columns of one (logits)
-  static constexpr int kSlots = kMode == kLse ? 0 : kMode == kDz ? 1 : 2;  // staging blocks of one
+  // Staging blocks of one.  A pair's gradient tiles are long: a sixth stage
+  // gives more than a second block (1-2 % at 256 to 1024 rows).
+  static constexpr int kSlots = kMode == kLse ? 0 : kMode == kGrad && !kPair ? 2 : 1;
   static constexpr uint32_t kBTile = kTN / kCtas * kBK * 2;
   static constexpr uint32_t kStage = kATile + kBTile;
-  static constexpr int kStages = kMode == kLse && !kPair ? 6 : kPair || kMode == kDz ? 5 : 3;
+  static constexpr int kStages =
+      kPair ? (kMode == kGrad ? 6 : 5) : kMode == kLse ? 6 : kMode == kDz ? 5 : 3;
   static constexpr uint32_t kOut = kEpi * kSlots * 4096;   // 32 x 128 B staging blocks
   static constexpr uint32_t kSmem = 1024 + kStages * kStage + kOut;
   static constexpr int kThreads = 64 + 32 * kEpi;
@@ -664,10 +667,15 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
         for (int m = 0; m < blocks; ++m) s += a.dbp[(size_t)m * a.Vp + v];
         if (a.v0 + v < a.V) a.dbias[a.v0 + v] = s * dlref;
       }
-      // The next staging slot, once the store before last has read it.
+      // The next staging slot, once the store that used it has read it.
       auto next_slot = [&]() {
-        slot ^= 1;
-        if (lane == 0) bulk_wait_read_but_one();
+        slot = C::kSlots - 1 - slot;
+        if (lane == 0) {
+          if (C::kSlots > 1)
+            bulk_wait_read_but_one();
+          else
+            bulk_wait_read_all();
+        }
         __syncwarp();
         return rowp + slot * 4096;
       };
