@@ -27,8 +27,8 @@
 // What bounds it, measured on a B200.  Many rows: the tensor cores, and over
 // longer runs the power limit (clocks settle near 1.3 GHz): the forward of
 // 8192 x 1024 x 50021 takes 599 us back to back (1400 TFLOP/s; one cuBLAS
-// product of that size, which also writes its logits, 714), its gradients 2234
-// (1127 TFLOP/s over three products).  Few rows: reading W and writing dW, then
+// product of that size, which also writes its logits, 714), its gradients 2190
+// (1150 TFLOP/s over three products).  Few rows: reading W and writing dW, then
 // the launches' own latencies: 13 rows of 768 x 30011 20 us (46 MB; 7 at a
 // copy's rate), the gradients of 77 rows 55 (94 MB; 14.5).
 //
@@ -37,7 +37,14 @@
 // tensor-core operands it multiplies;
 // dloss enters it relative to the largest |dloss| and that factor is applied
 // in fp32 at the end, so for equal dloss a dz near -1 (a label of low
-// probability) is exact and no rounding is shared by all rows.
+// probability) is exact and no rounding is shared by all rows.  Up to 64 rows
+// the rounding of a label's dz would still be that of whole rows of dh and dW
+// (errors of 0.38 % where rounding the results gives 0.17).  There dz is held
+// in two parts, the second being what rounding left of the first, as further
+// rows (from `low` on, 32 or 64): dW's K runs over both with h packed twice,
+// and dh's rows are summed in pairs.  A tile has room for 128 rows, so the
+// gradients of 1 and of 64 rows take 47.7 and 51.3 us where bf16 alone took
+// 44.3 and 46.1.
 #include "layer.cuh"
 
 namespace bb {
@@ -91,6 +98,7 @@ struct Info {
   int pad[15];
   int rows;      // rows with a label
   int direct;    // 1: every row has one, h is read where it lies
+  int low;       // backward, dz in two parts: first row of the second; else 0
   float dlref;   // largest |dloss| of those rows (1 when that is 0 or not finite)
 };
 
@@ -109,6 +117,7 @@ struct CeArgs {
   const float* dls;    //   dloss / dlref,
   const float* zl;     //   logit of the label (rows_kernel)
   float2* part;        // [Plan::runs][Np] (max, sum of exponentials)
+  uint16_t* dz;        // [Vp / 64][Np][64]
   float* dbp;          // [Np / 128][Vp] column sums of dz, or null
   float* dbias;        // [V], with dbp
 };
@@ -347,8 +356,9 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
   const uint32_t tmem = tmem_base_sh;
   grid_launch_dependents();
   grid_wait();
-  const int rows = a.info->rows;
-  const CUtensorMap* mapH = a.info->direct ? &tmH : &tmHp;
+  const int low = kMode == kLse ? 0 : a.info->low;
+  const int rows = kMode == kGrad && low ? 2 * low : a.info->rows;
+  const CUtensorMap* mapH = a.info->direct && !(kMode == kGrad && low) ? &tmH : &tmHp;
   const Work<kMode, kPair> work(a, rows, blockIdx.x / C::kCtas, gridDim.x / C::kCtas);
 
   if (warp == 0) {
@@ -527,6 +537,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
           mbar_arrive(&bars.acc_empty[acc]);
       }
     };
+    const int hi_rows = low ? low : 2 * kBM;  // kDz: rows of dz, or of its first part
     int slot = 0;  // kGrad: staging slot of the latest store
     float m = -INFINITY, s = 0.f;  // kLse: maximum and sum of exponentials
     uint32_t tc = 0;
@@ -631,7 +642,23 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
                              pack_bf16(z[4 * ch + 1].x, z[4 * ch + 1].y),
                              pack_bf16(z[4 * ch + 2].x, z[4 * ch + 2].y),
                              pack_bf16(z[4 * ch + 3].x, z[4 * ch + 3].y));
-            if (c & 32) {
+            if (low > r0) {
+              // What the rounding left (an infinity leaves nothing).
+              uint32_t u[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t k = pack_bf16(z[e].x, z[e].y);
+                const float x = __uint_as_float(k << 16), y = __uint_as_float(k & 0xFFFF0000u);
+                u[e] = pack_bf16(z[e].x == x ? 0.f : z[e].x - x, z[e].y == y ? 0.f : z[e].y - y);
+              }
+              uint4* out = reinterpret_cast<uint4*>(
+                  a.dz + ((size_t)((j.n0 + cbeg + c) / 64) * a.Np + low + r0 + lane) * 64 + (c & 32));
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                out[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+            }
+            // (The rows from `low` on are the second part's.)
+            if ((c & 32) && r0 < hi_rows) {
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
@@ -775,6 +802,8 @@ struct RowsArgs {
 };
 
 constexpr int kRowsThreads = 256;
+constexpr int kTwice = 64;  // the most rows whose dz is held in two parts: a tile's half
+static_assert(2 * kTwice <= kBM, "both parts in one tile, and in Np rows");
 
 __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
   const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
@@ -846,14 +875,16 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
     big = fmaxf(big, mx[w]);
   }
   const float dlref = big > 0.f && big < INFINITY ? big : 1.f;
+  const int low = kBwd && total <= kTwice ? (total + 31) / 32 * 32 : 0;
   if (blockIdx.x == 0 && tid == 0) {
     a.info->status = bad ? BB_ERR_BAD_LABEL : BB_OK;
     a.info->rows = total;
     a.info->direct = total == a.N;
+    a.info->low = low;
     a.info->dlref = dlref;
   }
   const int chunks = a.D / 8;  // 16-byte pieces of a row
-  const bool pack = total != a.N;
+  const bool pack = low || total != a.N;
   for (int r0 = 0; r0 < a.per_block; r0 += 32) {
     if (warp == 0) {
       const int n = r0 + lane < a.per_block ? base + r0 + lane : a.N;
@@ -902,6 +933,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
           if (c0 + 32 * i + lane < chunks) {
             s = dot8(x[i], y[i], s);
             if (pack) out[c0 + 32 * i + lane] = x[i];
+            if (low) out[(size_t)low * chunks + c0 + 32 * i + lane] = x[i];
           }
       }
 #pragma unroll
@@ -910,13 +942,16 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
     }
     __syncthreads();
   }
-  // The rest of the last 64 packed rows, which dW's last K step reads, is
-  // zero (times the zeros of dz).
-  if (pack && blockIdx.x == 0) {
-    const int end = (total + kBK - 1) / kBK * kBK;
+  // The packed rows behind the last (of either copy), up to the 64 of dW's last
+  // K step, are zero (times the zeros of dz).
+  if (pack) {
+    const int end = low ? low : (total + kBK - 1) / kBK * kBK;
     uint4* out = reinterpret_cast<uint4*>(a.hp);
-    for (size_t c = (size_t)total * chunks + tid; c < (size_t)end * chunks; c += kRowsThreads)
+    for (size_t c = (size_t)total * chunks + blockIdx.x * kRowsThreads + tid;
+         c < (size_t)end * chunks; c += (size_t)gridDim.x * kRowsThreads) {
       out[c] = make_uint4(0, 0, 0, 0);
+      if (low) out[(size_t)low * chunks + c] = make_uint4(0, 0, 0, 0);
+    }
   }
 }
 
@@ -963,9 +998,9 @@ __global__ void __launch_bounds__(256)
 }
 
 // Backward's end: dh rows rounded from the fp32 sums (0 where there is no
-// label).  A block takes 256 / kGroups pieces of eight columns; with several
-// parts per sum, kGroups threads share a piece's parts and their sums are
-// added in order.
+// label), of both parts of dz where it has two.  A block takes 256 / kGroups
+// pieces of eight columns; with several parts per sum, kGroups threads share a
+// piece's parts and their sums are added in order.
 template <int kGroups>
 __global__ void __launch_bounds__(256)
     dh_round_kernel(const Info* info, int N, int D, int Np, int splits, const int* pos,
@@ -979,13 +1014,19 @@ __global__ void __launch_bounds__(256)
   const int c = (int)(i % chunks) * 8;
   grid_launch_dependents();
   grid_wait();
-  const int p = live ? pos[n] : -1;
+  const int p = live ? pos[n] : -1, low = info->low;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (p >= 0) {
 #pragma unroll 4
     for (int s = g; s < splits; s += kGroups) {
       const float4* src = reinterpret_cast<const float4*>(acc + ((size_t)s * Np + p) * D + c);
-      const float4 x = src[0], y = src[1];
+      float4 x = src[0], y = src[1];
+      if (low) {
+        src = reinterpret_cast<const float4*>(acc + ((size_t)s * Np + low + p) * D + c);
+        const float4 lx = src[0], ly = src[1];
+        x.x += lx.x; x.y += lx.y; x.z += lx.z; x.w += lx.w;
+        y.x += ly.x; y.y += ly.y; y.z += ly.z; y.w += ly.w;
+      }
       v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
       v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
     }
@@ -1260,6 +1301,7 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   a.rlse = r.rlse;
   a.dls = r.dls;
   a.zl = r.zl;
+  a.dz = reinterpret_cast<uint16_t*>(ws + p.dz);
   a.dbp = dbias ? reinterpret_cast<float*>(ws + p.dbp) : nullptr;
   a.dbias = dbias;
   const int sms = sm_count();

@@ -140,6 +140,45 @@ def test_loss_and_gradients(N, D, V, share, bias):
     assert all(x is y or torch.equal(x, y) for x, y in zip(again, grads))
 
 
+@pytest.mark.parametrize("N,D,V,share,bias", [
+    (1, 288, 4321, 1.0, False), (5, 744, 753, 0.5, True), (7, 408, 42639, 0.5, True),
+    (63, 64, 300, 1.0, False), (64, 768, 5003, 1.0, True), (100, 200, 2001, 0.3, True),
+    (900, 136, 1999, 0.05, True)])
+def test_few_rows_are_as_exact_as_their_rounding(N, D, V, share, bias):
+    """Up to 64 rows with a label, dz is carried in two bf16 parts, the second
+    the rest of the first: 2^-16 of it is left, not 2^-8.  Otherwise the
+    bounds of the general case, and of dbias.  Weights spread over a factor of
+    256 let single rows lead."""
+    h, w, b, labels, _ = _general(N, D, V, share, bias, N + V)
+    labels[N // 2] = V // 3
+    g = torch.Generator().manual_seed(N)
+    dl = torch.exp2(8 * torch.rand(N, generator=g))
+    c = lambda t: None if t is None else t.cuda()
+    loss, lse = bb.bb_linear_ce_fwd(c(h), c(w), c(b), c(labels))
+    dh, dw, db = bb.bb_linear_ce_bwd(c(h), c(w), c(b), c(labels), lse, c(dl),
+                                     workspace=_ws(N, D, V, 1))
+    rows = (labels >= 0).nonzero()[:, 0].cuda()
+    R = rows.numel()
+    assert 0 < R <= 64
+    d = lambda t: t.cuda().double()
+    hr, wd, lab = d(h)[rows], d(w), labels.cuda()[rows].long()
+    z = hr @ wd.t() + (0 if b is None else d(b))
+    ez = D * 2.0**-23 * (hr.abs() @ wd.abs().t())
+    l64, dlr = d(lse)[rows, None], d(dl)[rows, None]
+    p = (z - l64).exp()
+    e = ez + 2.0**-22 * (z - l64).abs() + 2.0**-21
+    dz = dlr * (p - torch.nn.functional.one_hot(lab, V))
+    A, Pe = dz.abs(), dlr * p * e
+    for got, x, left, K in ((d(dh)[rows], wd, lambda m: m, V),
+                            (d(dw), hr, lambda m: m.t(), 2 * R)):
+        want = left(dz) @ x
+        tol = (2.0**-8 * want.abs() + (2.0**-16 + K * 2.0**-23) * (left(A) @ x.abs())
+               + left(Pe) @ x.abs())
+        assert ((got - want).abs() <= tol).all()
+    if b is not None:
+        assert ((d(db) - dz.sum(0)).abs() <= (2 * R + 8) * 2.0**-23 * A.sum(0) + Pe.sum(0)).all()
+
+
 def test_against_the_oracle_and_differences():
     """The written-out oracle, and the loss's central differences along a few
     weights (h = 2^-3 on bf16 weights that are multiples of 2^-3, exact): the
