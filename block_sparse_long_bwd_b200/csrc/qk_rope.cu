@@ -25,9 +25,9 @@
 // barriers between warps.  Loading a few heads into registers instead took
 // 28.0 and 85.6 us where this takes 24.9 and 59.4 (forward of 4 x 16 x 4096
 // rows of q and k, gradients of 8 x 12 x 4096, bf16): 5.4 and 5.1 TB/s.  The
-// issue slots are then about 70 % busy (unpacking, the rotation, two sums over
-// the row), which bounds the gradients before HBM does; two heads at a time
-// took them from 65.8 us (and the fp32 ones of 12 x 5003 from 21.2 to 22.1).
+// issue slots of the forward are then 68 % busy, those of the gradients 59 %
+// (unpacking, the rotation, two sums over the row); two heads at a time took
+// the gradients from 65.8 us (and the fp32 ones of 12 x 5003 from 21.2 to 22.1).
 //
 // Angles: theta^(-2i / rot_dim) / 2 pi, a fraction of a turn per position, is
 // held as a 64-bit fixed-point number, so the product with the position
