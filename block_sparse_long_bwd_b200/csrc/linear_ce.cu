@@ -557,14 +557,14 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < C::kCols / 32; ++i) {
           const int v = a.v0 + j.n0 + cbeg + 32 * i + lane;
-          b[i] = v < a.V ? (a.bias ? __ldg(a.bias + v) : 0.f) : -INFINITY;
+          b[i] = v < a.V ? (a.bias ? a.bias[v] : 0.f) : -INFINITY;
         }
         if (live) {
-          lab = __ldg(a.lab + row);
-          zl = __ldg(a.zl + row);
+          lab = a.lab[row];
+          zl = a.zl[row];
           if (kMode == kDz) {
-            lse = __ldg(a.rlse + row);
-            dl = __ldg(a.dls + row);
+            lse = a.rlse[row];
+            dl = a.dls[row];
           }
         }
         __syncwarp();
@@ -841,8 +841,8 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
   const float4* dloss4 = reinterpret_cast<const float4*>(a.dloss);
 #pragma unroll 4
   for (int i = tid; i < a.N / 4; i += kRowsThreads) {
-    const int4 l = __ldg(labels4 + i);
-    const float4 d = kBwd ? __ldg(dloss4 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const int4 l = labels4[i];
+    const float4 d = kBwd ? dloss4[i] : make_float4(0.f, 0.f, 0.f, 0.f);
     count(4 * i, l.x, d.x);
     count(4 * i + 1, l.y, d.y);
     count(4 * i + 2, l.z, d.z);
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
   }
   if (tid < (a.N & 3)) {
     const int i = (a.N & ~3) + tid;
-    count(i, __ldg(a.labels + i), kBwd ? __ldg(a.dloss + i) : 0.f);
+    count(i, a.labels[i], kBwd ? a.dloss[i] : 0.f);
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) {
@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
   for (int r0 = 0; r0 < a.per_block; r0 += 32) {
     if (warp == 0) {
       const int n = r0 + lane < a.per_block ? base + r0 + lane : a.N;
-      const int l = n < a.N ? __ldg(a.labels + n) : -1;
+      const int l = n < a.N ? a.labels[n] : -1;
       const bool live = l >= 0 && l < a.V;
       const unsigned m = __ballot_sync(0xffffffffu, live);
       const int p = before + __popc(m & ((1u << lane) - 1));
@@ -899,8 +899,8 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
         a.idx[p] = n;
         a.lab[p] = l;
         if (kBwd) {
-          a.rlse[p] = __ldg(a.lse + n);
-          a.dls[p] = __ldg(a.dloss + n) / dlref;
+          a.rlse[p] = a.lse[n];
+          a.dls[p] = a.dloss[n] / dlref;
         }
       }
       if (n < a.N) {
@@ -925,8 +925,8 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (c0 + 32 * i + lane < chunks) {
-            x[i] = __ldg(src + c0 + 32 * i + lane);
-            y[i] = __ldg(wl + c0 + 32 * i + lane);
+            x[i] = src[c0 + 32 * i + lane];
+            y[i] = wl[c0 + 32 * i + lane];
           }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
       }
 #pragma unroll
       for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-      if (lane == 0) a.zl[p] = s + (a.bias ? __ldg(a.bias + lab[r]) : 0.f);
+      if (lane == 0) a.zl[p] = s + (a.bias ? a.bias[lab[r]] : 0.f);
     }
     __syncthreads();
   }

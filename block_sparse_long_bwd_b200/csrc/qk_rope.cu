@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kQkThreads, kBwd ? 2 : 3)
 #pragma unroll
     for (int i = 0; i < R::kDepth - 1; ++i) fetch();
 
-    const int pos = a.pos ? __ldg(a.pos + tok) : l;
+    const int pos = a.pos ? a.pos[tok] : l;
     float2 c[2], s[2];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -331,10 +331,10 @@ __global__ void __launch_bounds__(kQkThreads, kBwd ? 2 : 3)
         dga[e] = dgb[e] = both(0.f);
         if (a.gamma[t]) {
           const float* g = a.gamma[t];
-          ga[e] = make_float2(__ldg(g + comp_a<kMode>(a, p0 + 2 * e)),
-                              __ldg(g + comp_a<kMode>(a, p0 + 2 * e + 1)));
-          gb[e] = make_float2(__ldg(g + comp_b<kMode>(a, p0 + 2 * e)),
-                              __ldg(g + comp_b<kMode>(a, p0 + 2 * e + 1)));
+          ga[e] = make_float2(g[comp_a<kMode>(a, p0 + 2 * e)],
+                              g[comp_a<kMode>(a, p0 + 2 * e + 1)]);
+          gb[e] = make_float2(g[comp_b<kMode>(a, p0 + 2 * e)],
+                              g[comp_b<kMode>(a, p0 + 2 * e + 1)]);
         }
       }
       // Forward: y_a = r (x_a (ga c) - x_b (gb s)), y_b = r (x_b (gb c) + x_a (ga s)).
