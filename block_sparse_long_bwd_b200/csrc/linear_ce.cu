@@ -45,6 +45,7 @@
 // and dh's rows are summed in pairs.  A tile has room for 128 rows, so the
 // gradients of 1 and of 64 rows take 47.7 and 51.3 us where bf16 alone took
 // 44.3 and 46.1.
+#include "ce_runs.h"
 #include "layer.cuh"
 
 namespace bb {
@@ -52,6 +53,7 @@ namespace {
 
 using namespace sm100;
 
+constexpr int kSms = 148;                      // a B200's
 constexpr int kBM = 128, kBK = 64;             // rows of a CTA's tile, K step
 constexpr uint32_t kBox = 64 * 64 * 2;         // one 64 x 64 bf16 box: 8 KB
 constexpr uint32_t kATile = kBM * kBK * 2;     // 16 KB
@@ -120,6 +122,7 @@ struct CeArgs {
   uint16_t* dz;        // [Vp / 64][Np][64]
   float* dbp;          // [Np / 128][Vp] column sums of dz, or null
   float* dbias;        // [V], with dbp
+  int dw_start[kSms + 1];  // kGrad of single CTAs: first tile of dW of each
 };
 
 struct Bars {
@@ -144,8 +147,7 @@ struct Job {
 // it take `lead` more of the cheaper kind before that is dealt out to all, so
 // the workers end within about one cheap tile of each other.  Single CTAs take
 // their tiles of dh, then a run of dW's tiles, ordered by columns first so that
-// h's part is loaded once or twice; the runs are cut by the tiles' columns
-// (the last may have few) less what the tiles of dh cost.
+// h's part is loaded once or twice; the host cuts the runs (dw_runs).
 template <int kMode, bool kPair>
 struct Work {
   using C = Cfg<kMode, kPair>;
@@ -169,25 +171,9 @@ struct Work {
       dw_first = 0;
       na = nh;
       wm = nw / dn;
-      const int cols = (a.D + 63) / 64;  // 64-column blocks of dW's rows
       more = nh % stride;
-      // Shares in units of a 64-column block, a tile being its blocks and one
-      // for itself: x for the workers with one tile of dh more, x + d for the
-      // others.
-      const float d = more ? 5.f * ch / cw : 0.f, all = (float)wm * (cols + dn);
-      float x = (all - d * (stride - more)) / stride, y = x + d;
-      if (x < 0.f) {
-        x = 0.f;
-        y = all / (stride - more);
-      }
-      auto start = [&](int w) {  // first tile of worker w
-        const float b = w >= stride ? all : w <= more ? w * x : more * x + (w - more) * y;
-        const int n = min((int)(b / (5.f * wm)), dn - 1), blk = min(4, cols - 4 * n) + 1;
-        const int m = (int)((b - 5.f * n * wm) / blk + 0.5f);
-        return n * wm + min(m, wm);
-      };
-      dw0 = start(w);
-      dw1 = w + 1 >= stride ? wm * dn : start(w + 1);
+      dw0 = a.dw_start[w];
+      dw1 = a.dw_start[w + 1];
       return;
     }
     dw_first = cw > ch;
@@ -1074,7 +1060,7 @@ int make_plan(int N, int D, int V, int pass, Plan* p) {
   p->a_rows = N < kBM ? (int)up(N, 8) : kBM;
   // Pairs of (max, sum): of every 128 columns, or two of a single CTA.
   p->runs = (V + 127) / 128;
-  if (!p->pair) p->runs = 2 * (p->runs > 148 ? 148 : p->runs);
+  if (!p->pair) p->runs = 2 * (p->runs > kSms ? kSms : p->runs);
   // Pieces of equal size whose dz fits kPieceBytes (512 columns at least).
   size_t fit = kPieceBytes / 2 / p->Np / 256 * 256;
   fit = fit < 512 ? 512 : fit;
@@ -1084,7 +1070,7 @@ int make_plan(int N, int D, int V, int pass, Plan* p) {
   // dh has few tiles of a long K when there are few rows: cut K into the
   // fewest parts that keep a tile within a worker's share of the launch (each
   // part writes dh's rows once more, and the last launch reads them).
-  const int workers = p->pair ? 74 : 148;
+  const int workers = p->pair ? kSms / 2 : kSms;
   const long long dn = (D + 255) / 256, mt = p->Np / tm;
   const long long nw = (p->Vp + tm - 1) / tm * dn, cw = tile_cost((N + kBK - 1) / kBK);
   const int hks = p->Vp / kBK;
@@ -1140,16 +1126,21 @@ cudaError_t launch_gemm_as(const CeArgs& a, long long tiles, int sms, const CUte
                         C::kSmem, kPair, s, a, h, hp, w, dz, dw, dh);
 }
 
+// `a` by value: the launch's runs of dW are filled in.
 template <int kMode>
-cudaError_t launch_gemm(const Plan& p, const CeArgs& a, int sms, const CUtensorMap& h,
+cudaError_t launch_gemm(const Plan& p, CeArgs a, int sms, const CUtensorMap& h,
                         const CUtensorMap& hp, const CUtensorMap& w, const CUtensorMap& dz,
                         const CUtensorMap& dw, const CUtensorMap& dh, cudaStream_t s) {
   const int tm = p.pair ? 2 * kBM : kBM;
   const int tn = p.pair ? Cfg<kMode, true>::kTN : Cfg<kMode, false>::kTN;
-  const long long mt = p.Np / tm, dn = (a.D + tn - 1) / tn;
-  const long long tiles = kMode == kGrad
-                              ? mt * dn * p.splits + (a.vn + tm - 1) / tm * dn
-                              : mt * ((a.vn + tn - 1) / tn);
+  const long long mt = p.Np / tm, dn = (a.D + tn - 1) / tn, wm = (a.vn + tm - 1) / tm;
+  const long long nh = mt * dn * p.splits;
+  const long long tiles = kMode == kGrad ? nh + wm * dn : mt * ((a.vn + tn - 1) / tn);
+  if (kMode == kGrad && !p.pair)
+    // (Up to 128 rows are two K steps of dW at most: one cost.)
+    dw_runs((int)wm, (int)dn, (a.D + 63) / 64, nh,
+            tile_cost((a.vn + kBK - 1) / kBK / p.splits), tile_cost(kBM / kBK),
+            (int)(tiles < sms ? tiles : sms), a.dw_start);
   return p.pair ? launch_gemm_as<kMode, true>(a, tiles, sms, h, hp, w, dz, dw, dh, s)
                 : launch_gemm_as<kMode, false>(a, tiles, sms, h, hp, w, dz, dw, dh, s);
 }
@@ -1159,10 +1150,10 @@ cudaError_t launch_gemm(const Plan& p, const CeArgs& a, int sms, const CUtensorM
 int rows_per_block(int N) { return N <= 1024 ? 8 : 32 * ((N + 16383) / 16384); }
 
 int sm_count() {
-  int dev = 0, sms = 148;
+  int dev = 0, sms = kSms;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms < 148 ? sms : 148;  // the plan sizes by a B200's 148
+  return sms < kSms ? sms : kSms;  // the plan sizes by a B200's
 }
 
 }  // namespace
