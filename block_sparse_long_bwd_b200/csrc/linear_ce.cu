@@ -34,17 +34,29 @@
 //
 // dz lies in panels of 64 columns, [Vp / 64][Np][64], so that every box that is
 // stored or loaded is one piece of memory.  It is held in bf16, the type of the
-// tensor-core operands it multiplies;
-// dloss enters it relative to the largest |dloss| and that factor is applied
-// in fp32 at the end, so for equal dloss a dz near -1 (a label of low
-// probability) is exact and no rounding is shared by all rows.  Up to 64 rows
-// the rounding of a label's dz would still be that of whole rows of dh and dW
-// (errors of 0.38 % where rounding the results gives 0.17).  There dz is held
-// in two parts, the second being what rounding left of the first, as further
-// rows (from `low` on, 32 or 64): dW's K runs over both with h packed twice,
-// and dh's rows are summed in pairs.  A tile has room for 128 rows, so the
-// gradients of 1 and of 64 rows take 47.7 and 51.3 us where bf16 alone took
-// 44.3 and 46.1.
+// tensor-core operands it multiplies; dloss enters it relative to the largest
+// |dloss| and that factor is applied in fp32 at the end.
+//
+// A row of dz has one large entry, its label's, and rounding that one is
+// rounding whole rows of dh and dW (errors of 0.22 % at 70 and 512 rows where
+// rounding the results gives 0.17; the other entries' roundings average out
+// in either product).  So what bf16 leaves of it (`rest`, one fp32 per row) is
+// added back: rest x w[label] to the row of dh when that is rounded, rest x
+// h[row] to the label's row of dW, for words with at most kFix rows (more
+// average out too).  The rows of each word are listed under the first dz
+// launch.  Few rows make dW's tiles short and all epilogue: there the fp32
+// sums of a word that is a label go to memory and the last launch adds to them
+// and rounds (in the epilogue, waiting for the rows of h, 129 and 256 rows took
+// 58.4 and 60.5 us where this takes 53.5 and 56.2); many rows hide the wait
+// under the products.  It costs 1.6 us of 54 at 77 rows, 2 at 129 and 256, 3.5 of
+// 75.5 at 512, 2.5 of 123 at 1024, below 1 % from 4096 on.
+//
+// Up to 64 rows the other entries do not average out either (errors of 0.38 %).
+// There dz is held in two parts, the second being what rounding left of the
+// first, as further rows (from `low` on, 32 or 64): dW's K runs over both with
+// h packed twice, and dh's rows are summed in pairs.  A tile has room for 128
+// rows, so the gradients of 1 and of 64 rows take 47.7 and 51.3 us where bf16
+// alone took 44.3 and 46.1.
 #include "ce_runs.h"
 #include "layer.cuh"
 
@@ -59,6 +71,9 @@ constexpr uint32_t kBox = 64 * 64 * 2;         // one 64 x 64 bf16 box: 8 KB
 constexpr uint32_t kATile = kBM * kBK * 2;     // 16 KB
 constexpr int kResA = 5;                       // A stages beside a resident B (below)
 constexpr size_t kPieceBytes = 256u << 20;     // dz of one vocabulary piece
+constexpr int kFix = 4;                        // most rows of a word whose entries are exact
+constexpr int kSideRows = 1024;  // up to these rows the last launch adds what bf16 left to dW:
+                                // side by side, 256 rows 55.8 us (epilogue 60.5), 1024 128 (129)
 
 enum Mode { kLse = 0, kDz = 1, kGrad = 2 };
 
@@ -120,6 +135,12 @@ struct CeArgs {
   const float* zl;     //   logit of the label (rows_kernel)
   float2* part;        // [Plan::runs][Np] (max, sum of exponentials)
   uint16_t* dz;        // [Vp / 64][Np][64]
+  // Where dz is in one part (see the top):
+  float* rest;         // packed rows: what bf16 leaves of the label's dz
+  unsigned* word_bits; // [V / 32]: the words that are labels,
+  int *word_n, *word_rows;  // [V], [kFix][V]: and the packed rows that have them
+  float* side;         // [N][D], by the first row of a word's list: its sums of dW; or null
+  const uint16_t *h, *hp;   // rows of h as they lie, and packed (without side)
   float* dbp;          // [Np / 128][Vp] column sums of dz, or null
   float* dbias;        // [V], with dbp
   int dw_start[kSms + 1];  // kGrad of single CTAs: first tile of dW of each
@@ -280,6 +301,58 @@ __device__ __forceinline__ void put(float2 (&z)[16], int i, float x) {
   for (int e = 0; e < 16; ++e) {
     z[e].x = i == 2 * e ? x : z[e].x;
     z[e].y = i == 2 * e + 1 ? x : z[e].y;
+  }
+}
+
+// What bf16 leaves of x (of an infinity nothing).
+__device__ __forceinline__ float bf16_rest(float x) {
+  const float k = __uint_as_float(pack_bf16(0.f, x) & 0xFFFF0000u);
+  return x == k ? 0.f : x - k;
+}
+
+// Appends packed rows to their labels' lists, a row per lane.  rows_kernel has
+// cleared the bits, and the counts of the words that are labels (the other
+// words' counts and lists are whatever the workspace held).
+__device__ __forceinline__ void append_rows(const CeArgs& a, int row, int rows) {
+  const int v = row < rows ? a.lab[row] : -1, lane = threadIdx.x & 31;
+  const unsigned same = __match_any_sync(0xffffffffu, v);
+  const int leader = __ffs(same) - 1;
+  int at = 0;
+  if (v >= 0 && lane == leader) {
+    atomicOr(a.word_bits + v / 32, 1u << (v & 31));
+    at = atomicAdd(a.word_n + v, __popc(same));
+  }
+  at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1));
+  if (v >= 0 && at < kFix) a.word_rows[(size_t)at * a.V + v] = row;
+}
+
+// The n <= kFix rows of word v's list in order (the appends were not).
+__device__ __forceinline__ void word_rows(const int* lists, int V, int v, int n,
+                                          int (&p)[kFix]) {
+#pragma unroll
+  for (int k = 0; k < kFix; ++k) p[k] = k < n ? lists[(size_t)k * V + v] : 0x7FFFFFFF;
+#pragma unroll
+  for (int i = 1; i < kFix; ++i)
+#pragma unroll
+    for (int k = kFix - 1; k >= i; --k) {
+      const int lo = min(p[k - 1], p[k]), hi = max(p[k - 1], p[k]);
+      p[k - 1] = lo;
+      p[k] = hi;
+    }
+}
+
+// v += r times eight bf16 values; v as floats or as their bits.
+__device__ __forceinline__ void fma_to(float& v, float r, float x) { v = fmaf(r, x, v); }
+__device__ __forceinline__ void fma_to(uint32_t& v, float r, float x) {
+  v = __float_as_uint(fmaf(r, x, __uint_as_float(v)));
+}
+template <typename T>
+__device__ __forceinline__ void fma8(float r, const uint4& x, T* v) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    fma_to(v[2 * i], r, __uint_as_float(u[i] << 16));
+    fma_to(v[2 * i + 1], r, __uint_as_float(u[i] & 0xFFFF0000u));
   }
 }
 
@@ -526,11 +599,57 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
     const int hi_rows = low ? low : 2 * kBM;  // kDz: rows of dz, or of its first part
     int slot = 0;  // kGrad: staging slot of the latest store
     float m = -INFINITY, s = 0.f;  // kLse: maximum and sum of exponentials
+    const int r0 = rank * kBM + quarter * 32;  // this warp's first row in a tile
+    // This tile and, kGrad, the next two (a tile's place takes several
+    // divisions: each is worked out once).
+    struct Place {
+      int t;
+      Job j;
+    } at[3];
+    auto place = [&](Place& p, int i) {
+      p.t = work.tile(i);
+      if (p.t >= 0) p.j = work.job(a, p.t);
+    };
+    place(at[0], 0);
+    if (kMode == kGrad) {
+      place(at[1], 1);
+      place(at[2], 2);
+    }
+    // kGrad, dz in one part: which of the warp's words of a tile are labels,
+    // loaded two tiles ahead, and one tile ahead the first row of the lane's
+    // word if it is one, so that nothing waits for them.
+    const bool fix = kMode == kGrad && !low && rows > 0;
+    auto word_bits = [&](const Place& p) {
+      const int v = p.j.row0 + r0;
+      return p.t >= 0 && p.j.dw && v < a.V ? a.word_bits[v / 32] : 0u;
+    };
+    auto list_head = [&](unsigned bits, const Place& p) {
+      return (bits >> lane) & 1u ? a.word_rows[p.j.row0 + r0 + lane] : -1;
+    };
+    unsigned bits1 = 0;
+    int head1 = -1;  // of the next tile
+    if (fix) {
+      head1 = list_head(word_bits(at[0]), at[0]);
+      bits1 = word_bits(at[1]);
+    }
+    if (kMode == kDz && !low && !a.add)  // under the first tile's loads
+      for (int i = (blockIdx.x * C::kEpi + warp - 2) * 32; i < rows;
+           i += gridDim.x * C::kEpi * 32)
+        append_rows(a, i + lane, rows);
     uint32_t tc = 0;
-    for (int t; (t = work.tile(tc)) >= 0; ++tc) {
-      const Job j = work.job(a, t);
+    auto advance = [&]() {
+      ++tc;
+      if (kMode == kGrad) {
+        at[0] = at[1];
+        at[1] = at[2];
+        place(at[2], tc + 2);
+      } else {
+        place(at[0], tc);
+      }
+    };
+    for (; at[0].t >= 0; advance()) {
+      const Job j = at[0].j;
       const int acc = tc & 1;
-      const int r0 = rank * kBM + quarter * 32;  // this warp's first row in the tile
       const int row = j.m0 + r0 + lane;          // packed row (logits)
       const bool live = row < rows;
       const int cbeg = half * C::kCols;
@@ -557,6 +676,12 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < C::kCols / 32; ++i) bias_sh[warp - 2][32 * i + lane] = b[i];
         __syncwarp();
+      }
+      int head = -1;  // kGrad: first row of the lane's word's list
+      if (fix) {
+        head = head1;
+        head1 = list_head(bits1, at[1]);
+        bits1 = word_bits(at[2]);
       }
       if (!mbar_wait_warp(&bars.acc_full[acc], (tc >> 1) & 1, &abort_flag, status)) break;
       tc_fence_after();
@@ -607,7 +732,11 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
                                     make_float2(kLog2e, kLog2e));
               z[e] = mul2(make_float2(ex2(d.x), ex2(d.y)), make_float2(dl, dl));
             }
-            if ((unsigned)hot < 32u) put(z, hot, dl * (ex2((zl - lse) * kLog2e) - 1.f));
+            if ((unsigned)hot < 32u) {
+              const float x = dl * (ex2((zl - lse) * kLog2e) - 1.f);
+              put(z, hot, x);
+              if (!low) a.rest[row] = bf16_rest(x);
+            }
             // Rows past the last: exact zeros, whatever the accumulator held.
             if (!live) {
 #pragma unroll
@@ -708,6 +837,38 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::kThreads, 1)
         // last, have nothing to write.
         if (x >= a.D || (j.dw ? y >= a.V : j.m0 + r0 >= rows)) continue;
         if (j.dw) {
+          if (head >= 0) {
+            if (a.side) {
+              float* side = a.side + (size_t)head * a.D + x;
+#pragma unroll
+              for (int ch = 0; ch < 16; ++ch)
+                if (x + 4 * ch < a.D) {
+                  const uint32_t* src = ch < 8 ? v0 + 4 * ch : v1 + 4 * (ch - 8);
+                  *reinterpret_cast<uint4*>(side + 4 * ch) =
+                      make_uint4(src[0], src[1], src[2], src[3]);
+                }
+            } else {
+              const int n = a.word_n[y + lane];
+              int p[kFix];
+              if (n <= kFix) {
+                word_rows(a.word_rows, a.V, y + lane, n, p);
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) {
+                  int row = p[0];
+#pragma unroll
+                  for (int k = 1; k < kFix; ++k) row = i == k ? p[k] : row;
+                  const float r = a.rest[row];
+                  const uint4* src = reinterpret_cast<const uint4*>(
+                      (a.info->direct ? a.h : a.hp) + (size_t)row * a.D + x);
+#pragma unroll
+                  for (int ch = 0; ch < 8; ++ch)
+                    if (x + 8 * ch < a.D)
+                      fma8(r, src[ch], ch < 4 ? v0 + 8 * ch : v1 + 8 * (ch - 4));
+                }
+              }
+            }
+          }
+          __syncwarp();
           uint8_t* out = next_slot();
 #pragma unroll
           for (int ch = 0; ch < 8; ++ch) {
@@ -782,7 +943,8 @@ struct RowsArgs {
   const float* dloss;   // backward
   float *loss, *lse_out;  // forward: zeroed where there is no label
   Info* info;
-  int *idx, *pos, *lab;
+  int *idx, *pos, *lab, *word_n;
+  unsigned* word_bits;
   float *rlse, *dls, *zl;
   uint16_t* hp;         // packed rows of h
 };
@@ -887,6 +1049,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
         if (kBwd) {
           a.rlse[p] = a.lse[n];
           a.dls[p] = a.dloss[n] / dlref;
+          if (!low) a.word_n[l] = 0;
         }
       }
       if (n < a.N) {
@@ -928,6 +1091,10 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
     }
     __syncthreads();
   }
+  if (kBwd && !low)
+    for (int i = blockIdx.x * kRowsThreads + tid; i < (a.V + 31) / 32;
+         i += gridDim.x * kRowsThreads)
+      a.word_bits[i] = 0;
   // The packed rows behind the last (of either copy), up to the 64 of dW's last
   // K step, are zero (times the zeros of dz).
   if (pack) {
@@ -983,32 +1150,87 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+struct EndArgs {
+  const Info* info;
+  int N, D, V, Np, splits;
+  int word_blocks;      // blocks that finish words of dW, in front of dh's
+  const int *labels, *pos;
+  const int* lab;       // packed rows: label,
+  const float* rest;    //   what bf16 left of its dz
+  const int *word_n, *word_rows;
+  const float *acc, *side;
+  const uint16_t *h, *hp, *w;
+  uint16_t *dh, *dw;
+};
+
+__device__ __forceinline__ void store8(uint16_t* out, const float (&v)[8], float scale) {
+  *reinterpret_cast<uint4*>(out) =
+      make_uint4(pack_bf16(v[0] * scale, v[1] * scale), pack_bf16(v[2] * scale, v[3] * scale),
+                 pack_bf16(v[4] * scale, v[5] * scale), pack_bf16(v[6] * scale, v[7] * scale));
+}
+
+// Eight columns of dW of the word whose list packed row p heads, where the
+// list holds all its rows: the sums, and what bf16 left of each label's entry
+// times the row's h, in order (the appends were not), rounded once.
+__device__ __forceinline__ void finish_word(const EndArgs& a, int p, int c) {
+  const uint16_t* h = (a.info->direct ? a.h : a.hp) + c;
+  const int v = a.lab[p];
+  const float4* src = reinterpret_cast<const float4*>(a.side + (size_t)p * a.D + c);
+  const float4 x = src[0], y = src[1];
+  // This row's own part, loaded beside the rest of what p leads to: most
+  // often it is the only one.
+  const float r = a.rest[p];
+  const uint4 hr = *reinterpret_cast<const uint4*>(h + (size_t)p * a.D);
+  const int n = a.word_n[v], first = a.word_rows[v];
+  if (first != p || n > kFix) return;
+  float s[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  if (n == 1) {
+    fma8(r, hr, s);
+  } else {
+    int row[kFix];
+    word_rows(a.word_rows, a.V, v, n, row);
+#pragma unroll
+    for (int k = 0; k < kFix; ++k)
+      if (k < n)
+        fma8(a.rest[row[k]], *reinterpret_cast<const uint4*>(h + (size_t)row[k] * a.D), s);
+  }
+  store8(a.dw + (size_t)v * a.D + c, s, a.info->dlref);
+}
+
 // Backward's end: dh rows rounded from the fp32 sums (0 where there is no
-// label), of both parts of dz where it has two.  A block takes 256 / kGroups
-// pieces of eight columns; with several parts per sum, kGroups threads share a
-// piece's parts and their sums are added in order.
+// label), of both parts of dz where it has two; where it has one, with what
+// its rounding left of the label's entry times the label's weights.  A block
+// takes 256 / kGroups pieces of eight columns; with several parts per sum,
+// kGroups threads share a piece's parts and their sums are added in order.
 template <int kGroups>
-__global__ void __launch_bounds__(256)
-    dh_round_kernel(const Info* info, int N, int D, int Np, int splits, const int* pos,
-                    const float* acc, uint16_t* dh) {
+__global__ void __launch_bounds__(256) end_kernel(const EndArgs a) {
   constexpr int kPieces = 256 / kGroups;
   __shared__ float sh[kGroups > 1 ? kGroups : 1][kPieces][kGroups > 1 ? 9 : 1];
-  const int chunks = D / 8, piece = threadIdx.x % kPieces, g = threadIdx.x / kPieces;
-  const size_t i = (size_t)blockIdx.x * kPieces + piece;
-  const size_t n = i / chunks;
-  const bool live = n < (size_t)N;
-  const int c = (int)(i % chunks) * 8;
+  const int chunks = a.D / 8;
   grid_launch_dependents();
   grid_wait();
-  const int p = live ? pos[n] : -1, low = info->low;
+  if ((int)blockIdx.x < a.word_blocks) {
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (!a.info->low && i / chunks < (size_t)a.info->rows)
+      finish_word(a, (int)(i / chunks), (int)(i % chunks) * 8);
+    return;
+  }
+  const int piece = threadIdx.x % kPieces, g = threadIdx.x / kPieces;
+  const size_t i = (size_t)(blockIdx.x - a.word_blocks) * kPieces + piece;
+  const size_t n = i / chunks;
+  const bool live = n < (size_t)a.N;
+  const int c = (int)(i % chunks) * 8;
+  const int p = live ? a.pos[n] : -1, lab = live ? a.labels[n] : 0, low = a.info->low;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (p >= 0) {
+    // The label's part goes to a group that has the fewest others.
+    const bool label = !low && g == a.splits % kGroups;
 #pragma unroll 4
-    for (int s = g; s < splits; s += kGroups) {
-      const float4* src = reinterpret_cast<const float4*>(acc + ((size_t)s * Np + p) * D + c);
+    for (int s = g; s < a.splits; s += kGroups) {
+      const float4* src = reinterpret_cast<const float4*>(a.acc + ((size_t)s * a.Np + p) * a.D + c);
       float4 x = src[0], y = src[1];
       if (low) {
-        src = reinterpret_cast<const float4*>(acc + ((size_t)s * Np + low + p) * D + c);
+        src = reinterpret_cast<const float4*>(a.acc + ((size_t)s * a.Np + low + p) * a.D + c);
         const float4 lx = src[0], ly = src[1];
         x.x += lx.x; x.y += lx.y; x.z += lx.z; x.w += lx.w;
         y.x += ly.x; y.y += ly.y; y.z += ly.z; y.w += ly.w;
@@ -1016,6 +1238,8 @@ __global__ void __launch_bounds__(256)
       v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
       v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
     }
+    if (label)
+      fma8(a.rest[p], *reinterpret_cast<const uint4*>(a.w + (size_t)lab * a.D + c), v);
   }
   if (kGroups > 1) {
 #pragma unroll
@@ -1028,14 +1252,7 @@ __global__ void __launch_bounds__(256)
       for (int e = 0; e < 8; ++e) v[e] += sh[q][piece][e];
   }
   if (!live) return;
-  if (p >= 0) {
-    const float dlref = info->dlref;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= dlref;
-  }
-  *reinterpret_cast<uint4*>(dh + n * D + c) =
-      make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                 pack_bf16(v[6], v[7]));
+  store8(a.dh + n * a.D + c, v, p >= 0 ? a.info->dlref : 0.f);
 }
 
 // ---- host -------------------------------------------------------------------
@@ -1043,7 +1260,8 @@ __global__ void __launch_bounds__(256)
 struct Plan {
   bool pair;
   int Np, a_rows, pieces, Vp, splits, runs;
-  size_t idx, pos, lab, rlse, dls, zl, hp, part, dz, dh, dbp, total;  // byte offsets
+  size_t idx, pos, lab, rlse, dls, zl, rest, word_bits, word_n, word_rows, side, hp, part,
+      dz, dh, dbp, total;  // byte offsets
 };
 
 size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -1099,6 +1317,13 @@ int make_plan(int N, int D, int V, int pass, Plan* p) {
     p->pos = take((size_t)N * 4);
     p->rlse = take((size_t)N * 4);
     p->dls = take((size_t)N * 4);
+    if (N > kTwice) {  // (dz is in two parts otherwise)
+      p->rest = take((size_t)N * 4);
+      p->word_bits = take((size_t)(V + 31) / 32 * 4);
+      p->word_n = take((size_t)V * 4);
+      p->word_rows = take((size_t)V * kFix * 4);
+      if (N <= kSideRows) p->side = take((size_t)N * D * 4);
+    }
     p->dz = take((size_t)p->Np * p->Vp * 2);
     p->dh = take((size_t)p->splits * p->Np * D * 4);
     p->dbp = take((size_t)(p->Np / kBM) * p->Vp * 4);
@@ -1275,6 +1500,8 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   r.rlse = reinterpret_cast<float*>(ws + p.rlse);
   r.dls = reinterpret_cast<float*>(ws + p.dls);
   r.hp = reinterpret_cast<uint16_t*>(ws + p.hp);
+  r.word_n = reinterpret_cast<int*>(ws + p.word_n);
+  r.word_bits = reinterpret_cast<unsigned*>(ws + p.word_bits);
   if (launch_chained(rows_kernel<true>, (N + r.per_block - 1) / r.per_block, kRowsThreads, 0,
                      false, s, r) != cudaSuccess)
     return BB_ERR_CUDA;
@@ -1293,6 +1520,13 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   a.dls = r.dls;
   a.zl = r.zl;
   a.dz = reinterpret_cast<uint16_t*>(ws + p.dz);
+  a.rest = reinterpret_cast<float*>(ws + p.rest);
+  a.word_n = r.word_n;
+  a.word_rows = reinterpret_cast<int*>(ws + p.word_rows);
+  a.word_bits = r.word_bits;
+  a.side = N <= kSideRows ? reinterpret_cast<float*>(ws + p.side) : nullptr;
+  a.h = r.h;
+  a.hp = r.hp;
   a.dbp = dbias ? reinterpret_cast<float*>(ws + p.dbp) : nullptr;
   a.dbias = dbias;
   const int sms = sm_count();
@@ -1306,10 +1540,30 @@ int bb_linear_ce_bwd(int N, int hidden, int V, const void* h, const void* w, con
   }
   const size_t pieces = (size_t)N * (hidden / 8);
   const int groups = p.splits > 4 ? 8 : 1;
-  if (launch_chained(groups > 1 ? dh_round_kernel<8> : dh_round_kernel<1>,
-                     (unsigned)((pieces * groups + 255) / 256), 256, 0, false, s,
-                     (const Info*)a.info, N, hidden, p.Np, p.splits, (const int*)r.pos,
-                     (const float*)(ws + p.dh), static_cast<uint16_t*>(dh)) != cudaSuccess)
+  EndArgs e{};
+  e.info = a.info;
+  e.N = N;
+  e.D = hidden;
+  e.V = V;
+  e.Np = p.Np;
+  e.splits = p.splits;
+  e.word_blocks = N > kTwice && a.side ? (int)((pieces + 255) / 256) : 0;
+  e.labels = labels;
+  e.pos = r.pos;
+  e.lab = r.lab;
+  e.rest = a.rest;
+  e.word_n = a.word_n;
+  e.word_rows = a.word_rows;
+  e.acc = reinterpret_cast<const float*>(ws + p.dh);
+  e.side = a.side;
+  e.h = r.h;
+  e.hp = r.hp;
+  e.w = r.w;
+  e.dh = static_cast<uint16_t*>(dh);
+  e.dw = static_cast<uint16_t*>(dw);
+  if (launch_chained(groups > 1 ? end_kernel<8> : end_kernel<1>,
+                     e.word_blocks + (unsigned)((pieces * groups + 255) / 256), 256, 0, false, s,
+                     e) != cudaSuccess)
     return BB_ERR_CUDA;
   return BB_OK;
 }

@@ -377,11 +377,12 @@ BB_API int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void*
  *   dw[v][c] = sum_n dz[n][v] h[n][c],   dbias[v] = sum_n dz[n][v]
  * The logits are computed again, a piece of the vocabulary at a time: the
  * workspace holds dz of one piece (at most 256 MiB, 512 columns at least),
- * never of all.  dz is rounded to bf16 for the two products (up to 64 labelled
- * rows: held in two bf16 parts, about 16 bits; dbias is summed before any
- * rounding); sums are fp32 and dh, dw are rounded once.  dz is
- * held relative to the largest |dloss|: rows whose dloss is below 2^-100 of it
- * lose precision.
+ * never of all.  Sums are fp32 and dh, dw are rounded once; dbias is summed
+ * before any rounding of dz.  For the two products dz is rounded to bf16, except
+ * for its largest entries, the labels': those enter dh in fp32, and dw for words
+ * that at most 4 rows have as label.  Up to 64 labelled rows all of dz is
+ * held in two bf16 parts, about 16 bits.  dz is held relative to the largest
+ * |dloss|: rows whose dloss is below 2^-100 of it lose precision.
  *   lse      [N] fp32, device, as bb_linear_ce_fwd wrote it
  *   dh       [N][hidden] bf16, device (written)
  *   dw       [V][hidden] bf16, device (written)
