@@ -14,7 +14,9 @@
 // Forward: one GEMM over (row tile, vocabulary tile); the epilogue keeps, per
 // row, the maximum and the sum of exponentials of its columns of the tile, and
 // a small launch merges these pairs in a fixed order.  Logits live in tensor
-// memory and registers only.
+// memory and registers only.  Where the pairs would not fit a fixed workspace
+// (from N V = 2^32 on) the vocabulary goes by in pieces, each merged into one
+// running pair per row.
 //
 // Backward: the vocabulary goes by in pieces whose dz (bf16) fits a fixed
 // workspace.  Per piece, one GEMM launch computes the logits again and
@@ -70,7 +72,7 @@ constexpr int kBM = 128, kBK = 64;             // rows of a CTA's tile, K step
 constexpr uint32_t kBox = 64 * 64 * 2;         // one 64 x 64 bf16 box: 8 KB
 constexpr uint32_t kATile = kBM * kBK * 2;     // 16 KB
 constexpr int kResA = 5;                       // A stages beside a resident B (below)
-constexpr size_t kPieceBytes = 256u << 20;     // dz of one vocabulary piece
+constexpr size_t kPieceBytes = 256u << 20;     // dz, or (max, sum) pairs, of one vocabulary piece
 constexpr int kFix = 4;                        // most rows of a word whose entries are exact
 constexpr int kSideRows = 1024;  // up to these rows the last launch adds what bf16 left to dW:
                                 // side by side, 256 rows 55.8 us (epilogue 60.5), 1024 128 (129)
@@ -1109,21 +1111,31 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a) {
 }
 
 // Forward: merges the (max, sum) pairs of eight rows in a fixed order: 32
-// groups take every 32nd pair, then one warp's lanes their 32 results.
-__global__ void __launch_bounds__(256)
-    lse_merge_kernel(const Info* info, const float2* part, int runs, int Np, const float* zl,
-                     const int* idx, float* loss, float* lse) {
+// groups take every 32nd pair, then one warp's lanes their 32 results and, past
+// the first piece of the vocabulary, the pair of the pieces before; the last
+// piece's launch writes the results, the others that pair.
+struct MergeArgs {
+  const Info* info;
+  const float2* part;   // [runs][Np]
+  float2* before;       // [Np]
+  int runs, Np, first, last;
+  const float* zl;
+  const int* idx;
+  float *loss, *lse;
+};
+
+__global__ void __launch_bounds__(256) lse_merge_kernel(const MergeArgs a) {
   __shared__ float2 sh[8][33];
   const int r = threadIdx.x & 7, g = threadIdx.x >> 3;
   grid_launch_dependents();
   grid_wait();
-  const int rows = info->rows;
+  const int rows = a.info->rows;
   if ((int)blockIdx.x * 8 >= rows) return;
   const int row = blockIdx.x * 8 + r;
   float m = -INFINITY, s = 0.f;
 #pragma unroll 4
-  for (int i = g; i < runs; i += 32) {
-    const float2 p = part[(size_t)i * Np + row];
+  for (int i = g; i < a.runs; i += 32) {
+    const float2 p = a.part[(size_t)i * a.Np + row];
     const float mm = fmaxf(m, p.x);
     const float ref = mm == -INFINITY ? 0.f : mm;
     s = s * ex2((m - ref) * kLog2e) + p.y * ex2((p.x - ref) * kLog2e);
@@ -1134,19 +1146,24 @@ __global__ void __launch_bounds__(256)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int out = blockIdx.x * 8 + warp;
   if (out >= rows) return;
-  const float2 p = sh[warp][lane];
-  m = p.x;
+  const float2 p = sh[warp][lane], b = a.first ? make_float2(-INFINITY, 0.f) : a.before[out];
+  m = fmaxf(p.x, b.x);
 #pragma unroll
   for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
   const float ref = m == -INFINITY ? 0.f : m;
   s = p.y * ex2((p.x - ref) * kLog2e);
 #pragma unroll
   for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+  s += b.y * ex2((b.x - ref) * kLog2e);
   if (lane == 0) {
-    const float l = ref + logf(s);
-    const int n = idx[out];
-    lse[n] = l;
-    loss[n] = l - zl[out];
+    if (a.last) {
+      const float l = ref + logf(s);
+      const int n = a.idx[out];
+      a.lse[n] = l;
+      a.loss[n] = l - a.zl[out];
+    } else {
+      a.before[out] = make_float2(m, s);
+    }
   }
 }
 
@@ -1260,7 +1277,7 @@ __global__ void __launch_bounds__(256) end_kernel(const EndArgs a) {
 struct Plan {
   bool pair;
   int Np, a_rows, pieces, Vp, splits, runs;
-  size_t idx, pos, lab, rlse, dls, zl, rest, word_bits, word_n, word_rows, side, hp, part,
+  size_t idx, pos, lab, rlse, dls, zl, before, rest, word_bits, word_n, word_rows, side, hp, part,
       dz, dh, dbp, total;  // byte offsets
 };
 
@@ -1276,15 +1293,18 @@ int make_plan(int N, int D, int V, int pass, Plan* p) {
   // Few rows load a lower box of h; what the MMA reads below it reaches only
   // accumulator rows that nothing uses.
   p->a_rows = N < kBM ? (int)up(N, 8) : kBM;
-  // Pairs of (max, sum): of every 128 columns, or two of a single CTA.
-  p->runs = (V + 127) / 128;
-  if (!p->pair) p->runs = 2 * (p->runs > kSms ? kSms : p->runs);
-  // Pieces of equal size whose dz fits kPieceBytes (512 columns at least).
-  size_t fit = kPieceBytes / 2 / p->Np / 256 * 256;
+  // Pieces of equal size whose dz fits kPieceBytes (512 columns at least), or
+  // whose pairs of (max, sum) do, one for 128 columns (single CTAs: two each,
+  // however many columns).
+  size_t fit = pass == 1 ? kPieceBytes / 2 / p->Np / 256 * 256
+                         : (kPieceBytes / 8 / p->Np - 4) * 128 / 256 * 256;
   fit = fit < 512 ? 512 : fit;
+  if (pass == 0 && !p->pair) fit = V;
   p->pieces = (int)((V + fit - 1) / fit);
   p->Vp = (int)up((V + p->pieces - 1) / p->pieces, 256);
   p->pieces = (V + p->Vp - 1) / p->Vp;
+  p->runs = ((p->Vp < V ? p->Vp : V) + 127) / 128;
+  if (!p->pair) p->runs = 2 * (p->runs > kSms ? kSms : p->runs);
   // dh has few tiles of a long K when there are few rows: cut K into the
   // fewest parts that keep a tile within a worker's share of the launch (each
   // part writes dh's rows once more, and the last launch reads them).
@@ -1311,6 +1331,7 @@ int make_plan(int N, int D, int V, int pass, Plan* p) {
   p->zl = take((size_t)N * 4);
   p->hp = take((size_t)p->Np * D * 2);
   if (pass == 0) {
+    p->before = take((size_t)p->Np * 8);
     // Whole tiles write their runs, past V too.
     p->part = take(((size_t)p->runs + 4) * p->Np * 8);
   } else {
@@ -1438,7 +1459,6 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
   a.D = hidden;
   a.V = V;
   a.Np = p.Np;
-  a.vn = V;
   a.a_bytes = p.a_rows * 2 * kBK;
   a.info = r.info;
   a.bias = bias;
@@ -1446,12 +1466,25 @@ int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w, con
   a.part = reinterpret_cast<float2*>(ws + p.part);
   a.zl = r.zl;
   const int sms = sm_count();
-  if (!p.pair && p.runs > 2 * sms) p.runs = 2 * sms;
-  if (launch_gemm<kLse>(p, a, sms, tmH, tmHp, tmW, tmW, tmW, tmW, s) != cudaSuccess ||
-      launch_chained(lse_merge_kernel, (N + 7) / 8, 256, 0, false, s, (const Info*)a.info,
-                     (const float2*)a.part, p.runs, p.Np, (const float*)r.zl, (const int*)r.idx,
-                     loss, lse) != cudaSuccess)
-    return BB_ERR_CUDA;
+  MergeArgs m{};
+  m.info = a.info;
+  m.part = a.part;
+  m.before = reinterpret_cast<float2*>(ws + p.before);
+  m.Np = p.Np;
+  m.zl = r.zl;
+  m.idx = r.idx;
+  m.loss = loss;
+  m.lse = lse;
+  for (int i = 0; i < p.pieces; ++i) {
+    a.v0 = i * p.Vp;
+    a.vn = V - a.v0 < p.Vp ? V - a.v0 : p.Vp;
+    m.runs = p.pair ? (a.vn + 127) / 128 : p.runs < 2 * sms ? p.runs : 2 * sms;
+    m.first = i == 0;
+    m.last = i == p.pieces - 1;
+    if (launch_gemm<kLse>(p, a, sms, tmH, tmHp, tmW, tmW, tmW, tmW, s) != cudaSuccess ||
+        launch_chained(lse_merge_kernel, (N + 7) / 8, 256, 0, false, s, m) != cudaSuccess)
+      return BB_ERR_CUDA;
+  }
   return BB_OK;
 }
 

@@ -362,8 +362,9 @@ BB_API int bb_qk_norm_rope_bwd(const bb_qk_desc* desc, const void* q, const void
  *   w       [V][hidden] bf16, device;  bias [V] fp32, device, or NULL
  *   labels  [N] int32, device
  *   loss, lse [N] fp32, device (written)
- *   workspace device, >= bb_linear_ce_workspace_size(N, hidden, V, 0) bytes,
- *             16-byte aligned; its status word is read by bb_attn_check_status
+ *   workspace device, >= bb_linear_ce_workspace_size(N, hidden, V, 0) bytes
+ *             (N rows of h and at most 256 MiB of per-row sums), 16-byte
+ *             aligned; its status word is read by bb_attn_check_status
  * Requires hidden % 8 == 0, 64 <= hidden <= 65536, N <= 2^20 and V <= 2^24,
  * else BB_ERR_UNSUPPORTED; N, V >= 1. */
 BB_API int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void* w,
