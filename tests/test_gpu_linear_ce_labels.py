@@ -14,7 +14,8 @@ its argument); entries other than labels' are rounded to bf16 (2^-8 of them,
 next to nothing here); sums and the last scaling leave 2^-20 of the terms'
 magnitudes; results are rounded once (2^-8).  The labels' own entries are
 held in fp32, so nothing of theirs is rounded before: for dh in every row, for
-dW in words that at most four rows have as label (above, 2^-8 of the terms)."""
+dW in words that at most four rows have as label (above, 2^-8 of the terms).
+Up to 64 rows all entries are held in two bf16 parts, which leave 2^-16."""
 
 import pytest
 import torch
@@ -68,9 +69,11 @@ def _bounds(h, w, labels, lse, dl):
         dz, off = d * (p - hot), d * p * (2.0**-22 * (z - l).abs() + 2.0**-21)
         dh[part] = dz @ W
         dw += dz.t() @ H[part]
+        two = rows.numel() <= 64
         rest, a = (dz * (1 - hot)).abs() * 2.0**-8 + off, dz.abs()
-        th[part] = (rest + 2.0**-20 * a) @ W.abs()
-        tw += (rest + (2.0**-20 + 2.0**-8 * heavy) * a).t() @ H[part].abs()
+        a = a * (2.0**-20 + two * 2.0**-16)
+        th[part] = (rest + a) @ W.abs()
+        tw += (rest + a + 2.0**-8 * (heavy & (not two)) * dz.abs()).t() @ H[part].abs()
     return rows, dh, dw, 2.0**-8 * dh.abs() + th, 2.0**-8 * dw.abs() + tw
 
 
@@ -79,7 +82,7 @@ def _bounds(h, w, labels, lse, dl):
     (100, 3001, 70, 60), (128, 700, 128, 64), (128, 3001, 127, 3001), (129, 700, 129, 350),
     (300, 1537, 300, 192), (400, 8192, 130, 64), (1000, 3001, 65, 65), (1000, 700, 1000, 1),
     (2500, 8192, 2500, 8192), (2500, 8100, 1250, 2025), (40003, 7001, 40003, 7001),
-    (20000, 8192, 4000, 4096)])
+    (20000, 8192, 4000, 4096), (20000, 8192, 60, 60), (30000, 8192, 64, 40)])
 def test_labels_entries_are_held_exactly(N, V, labelled, words):
     h, w, labels, lse, dl = _case(N, V, labelled, words, N + V)
     ws = torch.full((bb.bb_linear_ce_workspace_size(N, D, V, 1),), 0xFF, dtype=torch.uint8,

@@ -60,3 +60,41 @@ def test_forward(N, V, labelled):
     # every word excluded: no distribution
     loss = bb.bb_linear_ce_fwd(h, w, torch.full_like(b, float("-inf")), labels)[0]
     assert torch.isnan(loss[rows]).all()
+
+
+@pytest.mark.parametrize("N,D,V,labelled", [
+    (40003, 64, 7001, 40003), (300000, 64, 1201, 300000), (100, 64, (1 << 20) + 700, 90),
+    (100, 72, (1 << 20) + 513, 50), (128, 64, (1 << 20) + 1, 128), (3000, 128, 300001, 50),
+    (20000, 200, 20001, 64), (9000, 136, 40001, 2000)])
+def test_exact_integer_gradients(N, D, V, labelled):
+    """Two to seven pieces, the last one ragged; every logit is 0 (h uses
+    features that w leaves at zero) and lse 0, so dz, dh, dw and dbias are sums
+    of small integers below 2^24: equal to them rounded once.  dz in one part
+    and in two."""
+    g = torch.Generator().manual_seed(N + V)
+    half = D // 2
+    h, w = torch.zeros(N, D), torch.zeros(V, D)
+    h[:, :half] = torch.randint(-2, 3, (N, half), generator=g).float()
+    w[:, half:] = torch.randint(-2, 3, (V, D - half), generator=g).float()
+    labels = torch.full((N,), -100, dtype=torch.int32)
+    on = torch.randperm(N, generator=g)[:labelled].sort().values
+    labels[on] = torch.randint(0, V, (labelled,), generator=g, dtype=torch.int32)
+    labels[on[0]], labels[on[-1]] = 0, V - 1
+    dl = torch.tensor([1.0, 2.0])[torch.randint(0, 2, (N,), generator=g)]
+    off = torch.ones(N, dtype=torch.bool)
+    off[on] = False
+    h[off], dl[off] = float("nan"), float("nan")
+    h, w, labels, dl, on = (t.cuda() for t in (h.bfloat16(), w.bfloat16(), labels, dl, on))
+    ws = _ws(N, D, V, 1)
+    dh, dw, db = bb.bb_linear_ce_bwd(h, w, torch.zeros(V, device="cuda"), labels,
+                                     torch.zeros(N, device="cuda"), dl, workspace=ws)
+    assert bb.bb_attn_check_status(ws) == 0
+    # dz = dl (1 - onehot): all ones less the labels' words
+    H, W, lab, d = h[on].double(), w.double(), labels[on].long(), dl[on].double()
+    want = torch.zeros(N, D, dtype=torch.float64, device="cuda")
+    want[on] = d[:, None] * (W.sum(0) - W[lab])
+    assert torch.equal(dh, want.float().bfloat16())
+    want = (d @ H).expand(V, D).clone().index_add_(0, lab, -d[:, None] * H)
+    assert torch.equal(dw, want.float().bfloat16())
+    want = d.sum().expand(V).clone().index_add_(0, lab, -d)
+    assert torch.equal(db, want.float())
