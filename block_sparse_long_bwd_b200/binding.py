@@ -422,10 +422,19 @@ def _current_stream_ptr(device):
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def _site(site):
+    """A site as given: ctypes would cut it to its 32 bits, and two sites
+    share their decisions."""
+    if not 0 <= site < 1 << 32:
+        raise ValueError("site must be in [0, 2^32)")
+    return site
+
+
 def bb_dropout_fwd(x, residual, rate, seed, site=0, out=None, stream=None):
     """Output dropout with the residual added (see include/bb_attn.h):
     x [...] bf16 or fp32, residual like x or None; returns out like x (out may
     be x or residual)."""
+    site = _site(site)
     code, device = _dtype_code(x, "x"), x.get_device()
     _dense(x, "x", x.dtype, device)
     if residual is not None:
@@ -441,6 +450,7 @@ def bb_dropout_fwd(x, residual, rate, seed, site=0, out=None, stream=None):
 def bb_dropout_bwd(dout, rate, seed, site=0, dx=None, stream=None):
     """Gradient of bb_dropout_fwd's x (its residual's is dout); dx may be
     dout."""
+    site = _site(site)
     code, device = _dtype_code(dout, "dout"), dout.get_device()
     _dense(dout, "dout", dout.dtype, device)
     with _scope(device, stream):
