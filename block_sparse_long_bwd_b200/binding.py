@@ -567,12 +567,20 @@ def _ce_workspace(workspace, N, hidden, V, pass_, h):
     return workspace
 
 
-def bb_linear_ce_fwd(h, w, bias, labels, loss=None, lse=None, workspace=None, stream=None):
+def _ce_check(workspace, device, what):
+    """Waits for the call and raises what its status word says."""
+    _check(lib().bb_attn_check_status(workspace.data_ptr(), _current_stream_ptr(device)), what)
+
+
+def bb_linear_ce_fwd(h, w, bias, labels, loss=None, lse=None, workspace=None, stream=None,
+                     check=False):
     """Softmax cross entropy of the vocabulary projection (see
     include/bb_attn.h): h [N, hidden] and w [V, hidden] bf16, bias [V] fp32 or
     None, labels [N] int32 (negative: no loss); returns loss, lse [N] fp32.
     workspace: uint8 of bb_linear_ce_workspace_size(N, hidden, V, 0) bytes, or
-    None (allocated here; its status word is then out of reach)."""
+    None (allocated here).  A label >= V gives its row no loss; check=True waits
+    for the call and raises BBError (BB_ERR_BAD_LABEL) for one, check=False
+    leaves it to bb_attn_check_status(workspace) (not under stream capture)."""
     N, hidden, V, device = _ce_tensors(h, w, bias, labels)
     with _scope(device, stream):
         loss, lse = _fp32(loss, "loss", N, h), _fp32(lse, "lse", N, h)
@@ -582,15 +590,18 @@ def bb_linear_ce_fwd(h, w, bias, labels, loss=None, lse=None, workspace=None, st
                                       workspace.data_ptr(),
                                       workspace.numel() * workspace.element_size(),
                                       _current_stream_ptr(device)), "bb_linear_ce_fwd")
+        if check:
+            _ce_check(workspace, device, "bb_linear_ce_fwd")
     return loss, lse
 
 
 def bb_linear_ce_bwd(h, w, bias, labels, lse, dloss, dh=None, dw=None, dbias=None,
-                     workspace=None, stream=None):
+                     workspace=None, stream=None, check=False):
     """Gradients of bb_linear_ce_fwd for upstream dloss [N] fp32: returns dh
     [N, hidden], dw [V, hidden] bf16 and dbias [V] fp32 (None where bias is
     None and no dbias was given).  workspace: uint8 of
-    bb_linear_ce_workspace_size(N, hidden, V, 1) bytes, or None."""
+    bb_linear_ce_workspace_size(N, hidden, V, 1) bytes, or None; check as in
+    bb_linear_ce_fwd."""
     N, hidden, V, device = _ce_tensors(h, w, bias, labels)
     _dense(lse, "lse", torch.float32, device, (N,))
     _dense(dloss, "dloss", torch.float32, device, (N,))
@@ -605,6 +616,8 @@ def bb_linear_ce_bwd(h, w, bias, labels, lse, dloss, dh=None, dw=None, dbias=Non
                                       workspace.data_ptr(),
                                       workspace.numel() * workspace.element_size(),
                                       _current_stream_ptr(device)), "bb_linear_ce_bwd")
+        if check:
+            _ce_check(workspace, device, "bb_linear_ce_bwd")
     return dh, dw, dbias
 
 

@@ -29,8 +29,9 @@
  *  - `stream` is a cudaStream_t (NULL = the legacy default stream).  Compute
  *    calls validate on the host, enqueue their kernels on `stream` and return
  *    without synchronising.  Launch errors are returned; faults detected by a
- *    kernel (a wait that ran out, a corrupt random table) are written to a
- *    status word at the start of the workspace, read by bb_attn_check_status.
+ *    kernel (a wait that ran out, a corrupt random table, a label outside the
+ *    vocabulary) are written to a status word at the start of the workspace,
+ *    read by bb_attn_check_status.
  *  - Calls are re-entrant and thread-safe (no global mutable state; the one
  *    exception is bb_attn_fwd_noalloc's built-in scratch, see there); two
  *    calls may share a workspace only if they are ordered on the GPU.
@@ -471,8 +472,8 @@ BB_API int bb_attn_fwd_noalloc(const bb_attn_desc* desc, const void* q,
 BB_API int bb_attn_noalloc_status(void* stream);
 
 /* Waits for `stream`, then returns the status word the last call that used
- * `workspace` left there (BB_OK, BB_ERR_TIMEOUT or BB_ERR_BAD_TABLE), or
- * BB_ERR_CUDA if the copy itself failed. */
+ * `workspace` left there (BB_OK, BB_ERR_TIMEOUT, BB_ERR_BAD_TABLE or
+ * BB_ERR_BAD_LABEL), or BB_ERR_CUDA if the copy itself failed. */
 BB_API int bb_attn_check_status(const void* workspace, void* stream);
 
 /* Static description of a status code (never NULL). */
