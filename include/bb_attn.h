@@ -25,7 +25,9 @@
  *  - Pointers named *_host are host memory; every other pointer is device
  *    memory of the current CUDA device.  The caller owns every buffer; the
  *    library allocates nothing on the call path and keeps no state between
- *    calls.  Device pointers must be 16-byte aligned.
+ *    calls.  Device pointers must be 16-byte aligned.  Outputs and the
+ *    workspace overlap neither the inputs nor one another, except where a
+ *    call says that an output may be one of its inputs.
  *  - `stream` is a cudaStream_t (NULL = the legacy default stream).  Compute
  *    calls validate on the host, enqueue their kernels on `stream` and return
  *    without synchronising.  Launch errors are returned; faults detected by a
