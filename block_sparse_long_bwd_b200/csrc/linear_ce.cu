@@ -30,9 +30,11 @@
 // longer runs the power limit (clocks settle near 1.3 GHz): the forward of
 // 8192 x 1024 x 50021 takes 599 us back to back (1400 TFLOP/s; one cuBLAS
 // product of that size, which also writes its logits, 714), its gradients 2190
-// (1150 TFLOP/s over three products).  Few rows: reading W and writing dW, then
-// the launches' own latencies: 13 rows of 768 x 30011 20 us (46 MB; 7 at a
-// copy's rate), the gradients of 77 rows 55 (94 MB; 14.5).
+// (1150 TFLOP/s over three products).  Few rows: 13 rows of 768 x 30011 take 20 us
+// a call (46 MB; 7 at a copy's rate), 13.6 of them in the products, whose 235
+// tiles are two rounds on 148 CTAs; the gradients of 77 rows of 776 x 30011 56
+// (94 MB; 14.5), 19 in the dz kernel and 33 in that of dW and dh, which read W
+// and write dW one after the other.
 //
 // dz lies in panels of 64 columns, [Vp / 64][Np][64], so that every box that is
 // stored or loaded is one piece of memory.  It is held in bf16, the type of the
@@ -74,8 +76,8 @@ constexpr uint32_t kATile = kBM * kBK * 2;     // 16 KB
 constexpr int kResA = 5;                       // A stages beside a resident B (below)
 constexpr size_t kPieceBytes = 256u << 20;     // dz, or (max, sum) pairs, of one vocabulary piece
 constexpr int kFix = 4;                        // most rows of a word whose entries are exact
-constexpr int kSideRows = 1024;  // up to these rows the last launch adds what bf16 left to dW:
-                                // side by side, 256 rows 55.8 us (epilogue 60.5), 1024 128 (129)
+constexpr int kSideRows = 1024;  // up to these rows the last launch adds what bf16 left to dW,
+                                // above the epilogue (256 rows 56 and 60.5 us, 1024 128 and 129)
 
 enum Mode { kLse = 0, kDz = 1, kGrad = 2 };
 

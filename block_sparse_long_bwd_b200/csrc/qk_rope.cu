@@ -24,7 +24,8 @@
 // into shared memory (cp.async, 16 bytes a lane), without registers or
 // barriers between warps.  Loading a few heads into registers instead took
 // 28.0 and 85.6 us where this takes 24.9 and 59.4 (forward of 4 x 16 x 4096
-// rows of q and k, gradients of 8 x 12 x 4096, bf16): 5.4 and 5.1 TB/s.  The
+// rows of q and k, gradients of 8 x 12 x 4096, bf16, replayed in a graph; as
+// calls 25.9 and 62.5: 5.2 and 4.8 TB/s).  The
 // issue slots of the forward are then 68 % busy, those of the gradients 59 %
 // (unpacking, the rotation, two sums over the row); two heads at a time took
 // the gradients from 65.8 us (and the fp32 ones of 12 x 5003 from 21.2 to 22.1).
