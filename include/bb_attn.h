@@ -313,8 +313,8 @@ BB_API int bb_dropout_bwd(uint64_t n, int dtype, float rate, uint64_t seed, uint
  * fp32 arithmetic, rounded to the dtype once; the angle is reduced to one
  * turn exactly, so far positions are as accurate as near ones.  Squares are
  * summed in fp32: components below 2^60 and, with eps = 0, rows of 2^-60 or
- * more.  A row of zeros with eps = 0 has no norm (NaN), nor has one with an
- * infinity; neither reaches another row.
+ * more.  A row of zeros with eps = 0 and one with an infinity give NaN; no
+ * other row does for it, but the backward's gamma gradients may.
  *   eps     >= 0
  *   theta   >= 1 (ignored when rot_dim = 0); rot_dim even, 0 .. 64 */
 typedef struct {
@@ -384,12 +384,13 @@ BB_API int bb_linear_ce_fwd(int N, int hidden, int V, const void* h, const void*
  *   dw[v][c] = sum_n dz[n][v] h[n][c],   dbias[v] = sum_n dz[n][v]
  * The logits are computed again, a piece of the vocabulary at a time: the
  * workspace holds dz of one piece (at most 256 MiB, 512 columns at least),
- * never of all, a few copies of h and, above 64 rows, 20 bytes per word.  Sums are fp32 and dh, dw are rounded once; dbias is summed
- * before any rounding of dz.  For the two products dz is rounded to bf16, except
- * for its largest entries, the labels': those enter dh in fp32, and dw for words
- * that at most 4 rows have as label.  Up to 64 labelled rows all of dz is
- * held in two bf16 parts, about 16 bits.  dz is held relative to the largest
- * |dloss|: rows whose dloss is below 2^-100 of it lose precision.
+ * never of all, a few copies of h and, for N > 64, 20 bytes per word.  Sums are
+ * fp32 and dh, dw are rounded once; dbias is summed before any rounding of dz.
+ * For the two products dz is rounded to bf16, except for its largest entries,
+ * the labels': those enter dh in fp32, and dw for words that at most 4 rows have
+ * as label.  Up to 64 labelled rows all of dz is held in two bf16 parts, about
+ * 16 bits.  dz is held relative to the largest |dloss|: rows whose dloss is
+ * below 2^-100 of it lose precision.
  *   lse      [N] fp32, device, as bb_linear_ce_fwd wrote it
  *   dh       [N][hidden] bf16, device (written)
  *   dw       [V][hidden] bf16, device (written)
